@@ -56,10 +56,13 @@ extern "C" {
 #define SLIM_DEV_OVERFLOW 1 /* appending would exceed cap: sequence skipped, lens unchanged */
 #define SLIM_DEV_BADLEN 2   /* lens[b] < 0 or lens[b] > cap: sequence skipped */
 #define SLIM_DEV_TIMEOUT 4  /* a bounded in-kernel wait gave up (internal error) */
+#define SLIM_DEV_BADPAGE 8  /* a page number outside [0, num_pages) (paged caches; see slim_paged_cache) */
 
 /* Cache / weight element types. */
 #define SLIM_F32 0  /* fp32 storage, fp32 arithmetic */
 #define SLIM_BF16 1 /* bf16 storage, fp32 accumulation (tensor cores where the work is a contraction) */
+
+#define SLIM_E4M3 2 /* paged K+V caches only: 8-bit e4m3 storage, one fp32 scale per page and head */
 
 /* Decode orderings (section "K-Cache is All You Need", generation phase). */
 #define SLIM_AUTO 0      /* pick (a) or (b) from the measured table (slim_tune), default (b) */
@@ -256,6 +259,131 @@ size_t slim_mha_decode_workspace_bytes(int dtype, int B, int d, int H, int64_t c
 int slim_mha_decode_step(const float* q, const void* k_new, const void* v_new, void* Kcache, void* Vcache,
                          int32_t* lens, int dtype, int B, int d, int H, int64_t cap, float* out, void* workspace,
                          size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * slim_paged_cache — a K+V cache of one layer held in pages, for the models
+ * and layers that cannot run K-only: W_KV = W_K^(-1)·W_V needs a square W_K,
+ * which projections with fewer key heads than query heads do not have. In
+ * SLIM_E4M3 it holds a row in the bytes that the K-only cache needs in bf16.
+ * Beside slim_mha_decode_step (dense caches) in the family of standard
+ * attention over explicit keys and values; the reference's pages describe no
+ * paged or 8-bit cache, so everything here is this library's own reading.
+ *
+ * Row t of sequence b and key/value head h is row t % page of page
+ * table[b][t / page] of both pools. The struct is read on the host during the
+ * call; its pointers are device memory.
+ *
+ *   kpages, vpages  [num_pages][Hkv][page][dh] in `dtype`, 16-byte aligned.
+ *                   Keys are stored rotated (slim_mha_paged_append).
+ *   kscale, vscale  float[num_pages][Hkv] for SLIM_E4M3, NULL for SLIM_BF16:
+ *                   an element stands for its e4m3 value times the scale of
+ *                   its page and head. Scales are powers of two.
+ *   table           int32[B][max_pages]; entries past a sequence's rows are
+ *                   not read. Several sequences may read one page; a page that
+ *                   slim_mha_paged_append writes to must occur once.
+ *   num_pages, max_pages >= 1; num_pages*Hkv*page and max_pages*page < 2^31
+ *   dtype           SLIM_BF16 or SLIM_E4M3
+ *   B               1..4096 sequences;   Hkv 1..1024 key/value heads
+ *   dh              64 or 128;   page 16, 32, 64 or 128 rows
+ *
+ * The capacity of a sequence is cap = max_pages*page rows. In all calls below
+ * lens[b] counts the rows that sequence b had BEFORE the step; no call changes
+ * it, so that all layers of a step share it. Rows of several sequences come
+ * packed: sequence b owns rows starts[b] .. starts[b+1]-1 (int32[B+1], device)
+ * of [rows][heads][dh] arrays. Rows outside [starts[0], starts[B]) are neither
+ * read nor written.
+ *
+ * max_new is the caller's bound on starts[b+1]-starts[b] (0: `rows`); it sizes
+ * the launch. Device status, OR-ed into *dev_status: SLIM_DEV_BADLEN (lens[b]
+ * outside [0, cap], starts not ascending within [0, rows], more rows than
+ * max_new) and SLIM_DEV_OVERFLOW (lens[b] plus the new rows above cap) skip the
+ * sequence: nothing of it is written to the cache, and its output rows are
+ * zero (where its starts are valid). SLIM_DEV_BADPAGE: rows of that page are not written, and
+ * outputs that would read it are zero. Keys and values of attended rows must
+ * be finite; whatever lies in the pages behind a sequence's rows is never used.
+ *
+ * Return codes of all calls: SLIM_EINVAL for a null or misaligned pointer
+ * (16 bytes), a size out of range or head counts that do not divide;
+ * SLIM_EUNSUPPORTED for SLIM_F32, another dh, page or B > 4096.
+ */
+typedef struct slim_paged_cache {
+  void* kpages;
+  void* vpages;
+  float* kscale;
+  float* vscale;
+  const int32_t* table;
+  int64_t num_pages;
+  int dtype, B, Hkv, dh, page, max_pages;
+} slim_paged_cache;
+
+/*
+ * slim_mha_paged_append — writes the new rows of every sequence to the pages,
+ * row j of sequence b at position p = lens[b] + j, with the position rotation
+ * of the keys (and of the step's queries) applied on the way:
+ *     y_i = x_i·cos[p][i] - x_i'·sin[p][i],  y_i' = x_i'·cos[p][i] + x_i·sin[p][i]
+ * for i < rot/2, i' = i + rot/2 (interleaved = 0) or, with pairs of neighbours
+ * (interleaved = 1), the columns 2i and 2i+1; columns from `rot` on are copied.
+ *
+ * SLIM_BF16 stores the fp32 result rounded once. SLIM_E4M3: the scale of a
+ * page and head is the least power of two 2^e, -100 <= e <= 120, with
+ * amax <= 448·2^e over the rows of it that this call writes, or its present
+ * scale where that is larger and the page held rows of the sequence before
+ * (lens[b] lies inside the page). A larger scale re-rounds those older rows,
+ * which changes only values that become subnormal in e4m3 (below 2^-6 of the
+ * scale). New rows are rounded once. A key or value that is not finite makes
+ * the page's scale NaN, and with it what reads the page.
+ *
+ *   q        [rows][Hq][dh] bf16, row stride q_stride elements, or NULL
+ *   k, v     [rows][Hkv][dh] bf16, row strides k_stride, v_stride elements
+ *            (heads contiguous; strides multiples of 8, >= heads·dh)
+ *   cosines, sines  float[n_pos][rot/2], NULL with rot = 0
+ *   rot      0 or a multiple of 16, <= dh
+ *   n_pos    positions in the tables; lens[b] plus the new rows above it is
+ *            SLIM_DEV_OVERFLOW
+ *   q_out    [rows][Hq][dh] bf16 contiguous: the rotated queries; NULL exactly
+ *            when q is. May equal q where q is contiguous.
+ *   Hq       query heads (ignored without q)
+ *   rows     rows of the packed arrays; 0 returns SLIM_OK and launches nothing
+ */
+int slim_mha_paged_append(const slim_paged_cache* cache, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, const float* cosines,
+                          const float* sines, int rot, int interleaved, int64_t n_pos, const int32_t* starts,
+                          const int32_t* lens, int64_t rows, int64_t max_new, int Hq, void* q_out,
+                          int32_t* dev_status, void* stream);
+
+/*
+ * slim_mha_paged_gather — reads rows back: row j of sequence b at position
+ * first[b] + j, as bf16 (an e4m3 value times a power of two is exact in bf16
+ * above bf16's own underflow). For handing a sequence to another cache and
+ * for checks. first[b] plain positions; first[b] plus the rows above cap is
+ * SLIM_DEV_OVERFLOW. Rows are read whatever lens says: the caller asks for rows
+ * that were written.
+ *
+ *   k_out, v_out  [rows][Hkv][dh] bf16 contiguous
+ */
+int slim_mha_paged_gather(const slim_paged_cache* cache, const int32_t* starts, const int32_t* first, int64_t rows,
+                          int64_t max_new, void* k_out, void* v_out, int32_t* dev_status, void* stream);
+
+/*
+ * slim_mha_paged_decode — attention of one query row per sequence over the
+ * paged cache: out[b][i] = softmax(q_i·K_h^T/sqrt(dh))·V_h over rows
+ * 0 .. lens[b]+rows_extra-1, h = i / (Hq/Hkv).
+ *
+ *   q           [B][Hq][dh] bf16, row stride q_stride elements (rotated)
+ *   rows_extra  1 after slim_mha_paged_append of the step's row, 0 to attend
+ *               over lens[b] rows only (a fixed cache)
+ *   Hq          a multiple of Hkv
+ *   t_hint      host-side estimate of the longest attended length, used only
+ *               to choose how work is split (<= 0 means cap)
+ *   out         [B][Hq][dh] bf16 contiguous; zero for a sequence that was
+ *               skipped or has nothing to attend to
+ *   workspace   >= slim_mha_paged_decode_workspace_bytes(...), 256-byte
+ *               aligned; calls that share one must not overlap on the GPU
+ */
+size_t slim_mha_paged_decode_workspace_bytes(const slim_paged_cache* cache, int Hq);
+int slim_mha_paged_decode(const slim_paged_cache* cache, const void* q, int64_t q_stride, const int32_t* lens,
+                          int rows_extra, int Hq, int64_t t_hint, void* out, void* workspace, size_t ws_bytes,
+                          int32_t* dev_status, void* stream);
 
 /*
  * slim_tune — fills the SLIM_AUTO table for (dtype, B, d, H) by timing both

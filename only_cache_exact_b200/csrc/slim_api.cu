@@ -218,6 +218,8 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 }  // namespace
 
+void set_last_launch_count(int n) { g_last_launches = n; }
+
 cudaError_t launch_prefill_simt(const void* X, const void* W, void* kcache, const int32_t* lens, int dtype, int B,
                                 int n, int d, int64_t cap, cudaStream_t st, int* launches);
 cudaError_t launch_prefill_tc(const void* X, const void* W, void* kcache, const int32_t* lens, int B, int n, int d,
@@ -291,9 +293,10 @@ const char* slim_strerror(int code) {
     case SLIM_DEV_OVERFLOW: return "device: append would exceed cache capacity (sequence skipped)";
     case SLIM_DEV_BADLEN: return "device: length outside [0, cap] (sequence skipped)";
     case SLIM_DEV_TIMEOUT: return "device: a bounded wait gave up (internal error)";
+    case SLIM_DEV_BADPAGE: return "device: page number outside the pool (its rows not written, outputs reading it zero)";
     default: break;
   }
-  if (code > 0 && code < 8) return "device: several status bits set";
+  if (code > 0 && code < 16) return "device: several status bits set";
   return "unknown code";
 }
 

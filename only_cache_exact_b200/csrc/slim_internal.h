@@ -93,6 +93,35 @@ cudaError_t launch_prefill_attn(const void* Q, const void* kcache, const void* v
 cudaError_t launch_rows_gemm_tc(const void* A, const void* W, void* Y, const int32_t* lens, int rows_extra, int B,
                                 int d, int64_t cap, int32_t* status, cudaStream_t st, int* launches);
 
+// Paged K+V caches (slim_mha_paged_*).
+struct PagedAppendArgs {
+  const slim_paged_cache* cache;
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  const float* cosines;
+  const float* sines;
+  int rot, interleaved;
+  int64_t n_pos;
+  const int32_t* starts;
+  const int32_t* lens;
+  int64_t rows, max_new;
+  int Hq;
+  void* q_out;
+  int32_t* status;
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st, int* launches);
+cudaError_t launch_paged_gather(const slim_paged_cache& c, const int32_t* starts, const int32_t* first, int64_t rows,
+                                int64_t max_new, void* k_out, void* v_out, int32_t* status, cudaStream_t st,
+                                int* launches);
+size_t paged_decode_ws_bytes(const slim_paged_cache& c, int Hq);
+cudaError_t launch_paged_decode(const slim_paged_cache& c, const void* q, int64_t q_stride, const int32_t* lens,
+                                int rows_extra, int Hq, int64_t t_hint, void* out, void* workspace, int32_t* status,
+                                cudaStream_t st, int* launches);
+
 // Step front end: q = x·W_Q (fp32) and, with W_K, k = x·W_K (cache dtype) for B input rows.
 bool front_tc_supported(int dtype, int d);
 int front_tc_split(int d, bool with_k);  // cluster size of the tcgen05 front end

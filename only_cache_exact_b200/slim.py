@@ -20,8 +20,8 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 SLIM_OK, SLIM_EINVAL, SLIM_EWORKSPACE, SLIM_ECUDA, SLIM_EUNSUPPORTED = 0, -1, -2, -3, -4
-SLIM_DEV_OVERFLOW, SLIM_DEV_BADLEN, SLIM_DEV_TIMEOUT = 1, 2, 4
-SLIM_F32, SLIM_BF16 = 0, 1
+SLIM_DEV_OVERFLOW, SLIM_DEV_BADLEN, SLIM_DEV_TIMEOUT, SLIM_DEV_BADPAGE = 1, 2, 4, 8
+SLIM_F32, SLIM_BF16, SLIM_E4M3 = 0, 1, 2
 SLIM_AUTO, SLIM_VARIANT_A, SLIM_VARIANT_B = 0, 1, 2
 
 EXPORTS = [
@@ -31,6 +31,8 @@ EXPORTS = [
     "slim_mha_decode_workspace_bytes", "slim_mha_decode_step", "slim_debug_stall_next",
     "slim_prefill_attention_workspace_bytes", "slim_prefill_attention", "slim_project_qk",
     "slim_decode_step_x_workspace_bytes", "slim_decode_step_x", "slim_noalloc_scratch_bytes",
+    "slim_mha_paged_append", "slim_mha_paged_gather", "slim_mha_paged_decode_workspace_bytes",
+    "slim_mha_paged_decode",
 ]
 
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -65,6 +67,11 @@ _SIGS = {
     "slim_decode_step_x": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i64, _i32, _i64, _vp, _vp,
                                   _sz, _vp, _vp]),
     "slim_noalloc_scratch_bytes": (_sz, []),
+    "slim_mha_paged_append": (_i32, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i64, _vp, _vp, _i64,
+                                     _i64, _i32, _vp, _vp, _vp]),
+    "slim_mha_paged_gather": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "slim_mha_paged_decode_workspace_bytes": (_sz, [_vp, _i32]),
+    "slim_mha_paged_decode": (_i32, [_vp, _vp, _i64, _vp, _i32, _i32, _i64, _vp, _vp, _sz, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -266,6 +273,160 @@ def slim_mha_decode_step(q: torch.Tensor, k_new, v_new, Kcache: torch.Tensor, Vc
     _check(_lib.slim_mha_decode_step(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(Kcache), _ptr(Vcache), _ptr(lens),
                                      _DT[Kcache.dtype], B, d, H, cap, _ptr(out), _ptr(workspace), workspace.numel(),
                                      _ptr(status), _stream(stream)), "slim_mha_decode_step")
+
+
+class _PagedCacheC(ctypes.Structure):
+    """slim_paged_cache of include/slim.h."""
+    _fields_ = [("kpages", _vp), ("vpages", _vp), ("kscale", _vp), ("vscale", _vp), ("table", _vp),
+                ("num_pages", _i64), ("dtype", _i32), ("B", _i32), ("Hkv", _i32), ("dh", _i32), ("page", _i32),
+                ("max_pages", _i32)]
+
+
+class PagedKV:
+    """A K+V cache in pages (slim_paged_cache): kpages and vpages [num_pages][Hkv][page][dh] in bfloat16 or
+    float8_e4m3fn, for the latter kscale and vscale [num_pages][Hkv] float32, and table [B][max_pages] int32.
+    Holds the tensors; their contents may change, the tensors themselves are fixed."""
+
+    def __init__(self, kpages: torch.Tensor, vpages: torch.Tensor, table: torch.Tensor, kscale=None, vscale=None):
+        dt = {torch.bfloat16: SLIM_BF16, torch.float8_e4m3fn: SLIM_E4M3}.get(kpages.dtype)
+        if dt is None or kpages.dim() != 4 or vpages.shape != kpages.shape or vpages.dtype != kpages.dtype:
+            raise ValueError("kpages and vpages must be [num_pages][Hkv][page][dh] in bfloat16 or float8_e4m3fn")
+        if table.dim() != 2 or table.dtype != torch.int32:
+            raise ValueError("table must be int32 [B][max_pages]")
+        if (dt == SLIM_E4M3) != (kscale is not None) or (kscale is None) != (vscale is None):
+            raise ValueError("kscale and vscale go with float8_e4m3fn pages")
+        self.device = kpages.device
+        named = [(kpages, "kpages"), (vpages, "vpages"), (table, "table")]
+        if kscale is not None:
+            for t, nm in ((kscale, "kscale"), (vscale, "vscale")):
+                if t.shape != kpages.shape[:2] or t.dtype != torch.float32:
+                    raise ValueError(f"{nm} must be float32 [num_pages][Hkv]")
+                named.append((t, nm))
+        for t, nm in named:
+            _cuda(t, nm)
+            if t.device != self.device:
+                raise ValueError(f"{nm} is on another device")
+        self.kpages, self.vpages, self.table, self.kscale, self.vscale = kpages, vpages, table, kscale, vscale
+        self.dtype = dt
+        self.num_pages, self.Hkv, self.page, self.dh = kpages.shape
+        self.B, self.max_pages = table.shape
+        self._c = _PagedCacheC(kpages.data_ptr(), vpages.data_ptr(), None if kscale is None else kscale.data_ptr(),
+                               None if vscale is None else vscale.data_ptr(), table.data_ptr(), self.num_pages, dt,
+                               self.B, self.Hkv, self.dh, self.page, self.max_pages)
+        self._ref = ctypes.byref(self._c)
+
+    @property
+    def cap(self) -> int:
+        """Rows a sequence can have."""
+        return self.max_pages * self.page
+
+
+def _on_device(t, name: str, device, dtype, shape=None) -> int:
+    if t.device != device or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _packed_rows(t, name: str, device, heads, dh: int):
+    """(pointer, row stride) of a bfloat16 [rows][heads][dh] tensor whose rows may lie apart."""
+    if t.device != device or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != dh or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be bfloat16 [rows][{'heads' if heads is None else heads}][{dh}] on {device}")
+    s0, s1, s2 = t.stride()
+    width = t.shape[1] * dh
+    if s2 != 1 or (s1 != dh and t.shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (s0 if t.shape[0] > 1 else width)
+
+
+def _paged_call(fn, where: str, device, stream, *args) -> None:
+    """Calls fn(*args, stream) with `device` current: a launch goes to the current device whatever its stream."""
+    if torch.cuda.current_device() == device.index:
+        s = torch.cuda.current_stream() if stream is None else stream
+        code = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            code = fn(*args, s.cuda_stream)
+    if code != SLIM_OK:
+        raise SlimError(code, where)
+
+
+def slim_mha_paged_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor,
+                          status: torch.Tensor, q=None, q_out=None, cos=None, sin=None, interleaved: bool = False,
+                          max_new: int = 0, stream=None) -> None:
+    """Writes the packed rows k, v [rows][Hkv][dh] behind the lens[b] rows of every sequence; the keys (and
+    q [rows][Hq][dh] into q_out) are rotated by cos, sin [n_pos][rot/2] float32. lens is not changed."""
+    dev, rows = cache.device, k.shape[0]
+    kp, ks = _packed_rows(k, "k", dev, cache.Hkv, cache.dh)
+    vp, vs = _packed_rows(v, "v", dev, cache.Hkv, cache.dh)
+    if v.shape[0] != rows or (q is None) != (q_out is None) or (cos is None) != (sin is None):
+        raise ValueError("k and v need the same rows; q goes with q_out, cos with sin")
+    qp = qo = None
+    qs = Hq = 0
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qs = _packed_rows(q, "q", dev, Hq, cache.dh)
+        qo = _on_device(q_out, "q_out", dev, torch.bfloat16, (rows, Hq, cache.dh))
+        if q.shape[0] != rows:
+            raise ValueError("q and k need the same rows")
+    cp = sp = None
+    rot = n_pos = 0
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape[1] == 0:
+            raise ValueError("cos must be float32 [n_pos][rot/2]")
+        cp = _on_device(cos, "cos", dev, torch.float32)
+        sp = _on_device(sin, "sin", dev, torch.float32, cos.shape)
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    _paged_call(_lib.slim_mha_paged_append, "slim_mha_paged_append", dev, stream, cache._ref, qp, qs, kp, ks, vp, vs,
+                cp, sp, rot, 1 if interleaved else 0, n_pos,
+                _on_device(starts, "starts", dev, torch.int32, (cache.B + 1,)),
+                _on_device(lens, "lens", dev, torch.int32, (cache.B,)), rows, max_new, Hq, qo,
+                _on_device(status, "status", dev, torch.int32))
+
+
+def slim_mha_paged_gather(cache: PagedKV, first: torch.Tensor, starts: torch.Tensor, k_out: torch.Tensor,
+                          v_out: torch.Tensor, status: torch.Tensor, max_new: int = 0, stream=None) -> None:
+    """Rows first[b] .. of every sequence, starts[b+1]-starts[b] of them, packed as bfloat16 [rows][Hkv][dh]."""
+    dev, rows = cache.device, k_out.shape[0]
+    shape = (rows, cache.Hkv, cache.dh)
+    _paged_call(_lib.slim_mha_paged_gather, "slim_mha_paged_gather", dev, stream, cache._ref,
+                _on_device(starts, "starts", dev, torch.int32, (cache.B + 1,)),
+                _on_device(first, "first", dev, torch.int32, (cache.B,)), rows, max_new,
+                _on_device(k_out, "k_out", dev, torch.bfloat16, shape),
+                _on_device(v_out, "v_out", dev, torch.bfloat16, shape),
+                _on_device(status, "status", dev, torch.int32))
+
+
+def slim_mha_paged_decode_workspace_bytes(cache: PagedKV, Hq: int) -> int:
+    with torch.cuda.device(cache.device):
+        return int(_lib.slim_mha_paged_decode_workspace_bytes(cache._ref, Hq))
+
+
+def alloc_paged_decode_workspace(cache: PagedKV, Hq: int) -> torch.Tensor:
+    """Caller-owned scratch for slim_mha_paged_decode."""
+    n = slim_mha_paged_decode_workspace_bytes(cache, Hq)
+    if n == 0:
+        raise SlimError(SLIM_EINVAL, "slim_mha_paged_decode_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def slim_mha_paged_decode(cache: PagedKV, q: torch.Tensor, lens: torch.Tensor, out: torch.Tensor,
+                          workspace: torch.Tensor, status: torch.Tensor, rows_extra: int = 1, t_hint: int = 0,
+                          stream=None) -> None:
+    """Attention of one query row per sequence, q [B][Hq][dh] bfloat16, over rows 0 .. lens[b]+rows_extra-1;
+    out [B][Hq][dh] bfloat16."""
+    dev = cache.device
+    qp, qs = _packed_rows(q, "q", dev, None, cache.dh)
+    if q.shape[0] != cache.B:
+        raise ValueError("q must have one row per sequence")
+    _paged_call(_lib.slim_mha_paged_decode, "slim_mha_paged_decode", dev, stream, cache._ref, qp, qs,
+                _on_device(lens, "lens", dev, torch.int32, (cache.B,)), rows_extra, q.shape[1], t_hint,
+                _on_device(out, "out", dev, torch.bfloat16, q.shape),
+                _on_device(workspace, "workspace", dev, torch.uint8), workspace.numel(),
+                _on_device(status, "status", dev, torch.int32))
 
 
 def slim_decode_step_host(q_host: torch.Tensor, k_new_host, Kcache: torch.Tensor, lens: torch.Tensor,
