@@ -331,7 +331,7 @@ typedef struct slim_paged_cache {
  * (lens[b] lies inside the page). A larger scale re-rounds those older rows,
  * which changes only values that become subnormal in e4m3 (below 2^-6 of the
  * scale). New rows are rounded once. A key or value that is not finite makes
- * the page's scale NaN, and with it what reads the page.
+ * the page's scale NaN, and with it every output that attends a row of the page.
  *
  *   q        [rows][Hq][dh] bf16, row stride q_stride elements, or NULL
  *   k, v     [rows][Hkv][dh] bf16, row strides k_stride, v_stride elements
@@ -384,6 +384,27 @@ size_t slim_mha_paged_decode_workspace_bytes(const slim_paged_cache* cache, int 
 int slim_mha_paged_decode(const slim_paged_cache* cache, const void* q, int64_t q_stride, const int32_t* lens,
                           int rows_extra, int Hq, int64_t t_hint, void* out, void* workspace, size_t ws_bytes,
                           int32_t* dev_status, void* stream);
+
+/*
+ * slim_mha_paged_prefill — causal attention of the new rows of every sequence
+ * over the paged cache, after slim_mha_paged_append of them: query j of
+ * sequence b sits at position lens[b] + j and attends rows 0 .. lens[b]+j.
+ * Whole prompts, chunks behind cached rows and a few proposed tokens alike.
+ *
+ *   q          [rows][Hq][dh] bf16, row stride q_stride elements (rotated)
+ *   Hq         a multiple of Hkv, at most 128·Hkv
+ *   t_hint     host-side estimate of the longest lens[b] + new rows, used only
+ *              to choose how work is split (<= 0 means cap). The workspace call takes the
+ *              same value.
+ *   out        [rows][Hq][dh] bf16 contiguous
+ *   workspace  >= slim_mha_paged_prefill_workspace_bytes(...), 256-byte aligned
+ *              (may be NULL where that is 0)
+ */
+size_t slim_mha_paged_prefill_workspace_bytes(const slim_paged_cache* cache, int Hq, int64_t rows, int64_t max_new,
+                                              int64_t t_hint);
+int slim_mha_paged_prefill(const slim_paged_cache* cache, const void* q, int64_t q_stride, const int32_t* starts,
+                           const int32_t* lens, int64_t rows, int64_t max_new, int Hq, int64_t t_hint, void* out,
+                           void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /*
  * slim_tune — fills the SLIM_AUTO table for (dtype, B, d, H) by timing both

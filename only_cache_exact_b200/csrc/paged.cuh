@@ -70,6 +70,11 @@ __device__ __forceinline__ int scale_exponent(uint32_t amax_bits) {
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// Exponent of a scale (a power of two); NaN for a poisoned page.
+__device__ __forceinline__ float scale_log2(float s) {
+  return s != s ? s : static_cast<float>(static_cast<int>(__float_as_uint(s) >> 23) - 127);
+}
+
 // Two e4m3 codes (lo in the low byte), rounded to nearest even, saturating; NaN stays NaN.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));

@@ -119,4 +119,32 @@ int slim_mha_paged_decode(const slim_paged_cache* cache, const void* q, int64_t 
   return finish(e, launches);
 }
 
+size_t slim_mha_paged_prefill_workspace_bytes(const slim_paged_cache* cache, int Hq, int64_t rows, int64_t max_new,
+                                              int64_t t_hint) {
+  if (check_cache(cache) != SLIM_OK || Hq < 1 || Hq % cache->Hkv || Hq / cache->Hkv > 128 || rows < 1 ||
+      rows > kInt32Max || max_new < 0)
+    return 0;
+  return paged_prefill_ws_bytes(*cache, Hq, rows, max_new == 0 ? rows : std::min(max_new, rows), t_hint);
+}
+
+int slim_mha_paged_prefill(const slim_paged_cache* cache, const void* q, int64_t q_stride, const int32_t* starts,
+                           const int32_t* lens, int64_t rows, int64_t max_new, int Hq, int64_t t_hint, void* out,
+                           void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  const int rc = check_cache(cache);
+  if (rc != SLIM_OK) return rc;
+  if (rows == 0) return finish(cudaSuccess, 0);
+  if (!out || !aligned(out, 16) || !dev_status) return SLIM_EINVAL;
+  if (Hq < 1 || Hq > 8192 || Hq % cache->Hkv || !check_rows(q, q_stride, Hq, cache->dh)) return SLIM_EINVAL;
+  if (!check_packed(starts, lens, rows, max_new, Hq)) return SLIM_EINVAL;
+  if (Hq / cache->Hkv > 128) return SLIM_EUNSUPPORTED;
+  if (!paged_prefill_fits(*cache, Hq, rows, max_new, t_hint)) return SLIM_EINVAL;
+  const size_t need = paged_prefill_ws_bytes(*cache, Hq, rows, max_new, t_hint);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || ws_bytes < need)) return SLIM_EWORKSPACE;
+  int launches = 0;
+  const cudaError_t e =
+      launch_paged_prefill(*cache, q, q_stride, starts, lens, rows, max_new, Hq, t_hint, out, workspace, dev_status,
+                           static_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
 }  // extern "C"

@@ -93,7 +93,9 @@ __device__ __forceinline__ void load_unit(const __nv_bfloat16* src, int e0, int 
 __device__ __forceinline__ uint4 pack8_bf16(const float* x) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
+// Codes of 8 values; zeros under a NaN scale, so that only the scale carries it.
 __device__ __forceinline__ uint2 pack8_e4m3(const float* x, float inv) {
+  if (inv != inv) return make_uint2(0u, 0u);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = to_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);

@@ -4,9 +4,10 @@
 // Mathematics, per sequence and key/value head, for the G query heads that
 // share it: s_t = q·K_t·log2(e)/sqrt(dh), m = max s, p_t = 2^(s_t - m),
 // o = Σ p_t V_t / Σ p_t, kept as a running (m, l, o) per warp and joined by
-// 2^(m_i - m). In e4m3 K_t = ks·k8_t and V_t = vs·v8_t with scales of the page
-// and head: ks multiplies the score; the p·V sum runs on v8 in units of the
-// largest value scale met so far, p·(vs/vref), an exact factor.
+// 2^(m_i - m). In e4m3 K_t = ks·k8_t and V_t = 2^lv·v8_t with scales of the page
+// and head: ks multiplies the score, and the weights of the sum over v8 are
+// P_t = 2^(s_t + lv - m) with m the running maximum of s + lv, which keeps them
+// in f16's range whatever the pages' scales are; l adds P_t·2^-lv.
 //
 // Bound: memory. Each cached element is read once and meets 4·G flops per 2 or
 // 1 bytes; the row count of every matrix product is 8 or 16 (padded heads), so
@@ -17,8 +18,8 @@
 // probabilities go from the result's layout to the operand's by movmatrix,
 // without shared memory. e4m3 codes become f16 pairs exactly (one cvt per
 // pair), with the query scaled into f16's range by a power of two per head.
-// Probabilities are rounded to f16 (2^-12) for e4m3; for bf16 values they are
-// split in two bf16 parts (2^-17), since one part (2^-9) would be the largest
+// Probabilities are rounded to f16 (2^-11) for e4m3; for bf16 values they are
+// split in two bf16 parts (2^-16), since one part (2^-8) would be the largest
 // error of the whole step.
 //
 // Work split: 16-row tiles of all (sequence, head group) pairs on one line, cut
@@ -369,7 +370,6 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
-    float vref = 0.f;
     bad = false;
 
     for (int t = sg.tile; t < sg.end; t += C::kTT) {
@@ -414,11 +414,11 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
       float mx[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-      float vs[C::kTT];
+      float lv[C::kTT];
 #pragma unroll
       for (int k = 0; k < C::kTT; ++k) {
         const float ks = E && k < tiles ? my_scale[(stage * C::kTT + k) * 2] : 1.f;
-        vs[k] = E && k < tiles ? my_scale[(stage * C::kTT + k) * 2 + 1] : 0.f;
+        lv[k] = E && k < tiles ? scale_log2(my_scale[(stage * C::kTT + k) * 2 + 1]) : 0.f;
         const int r0 = (t + k) * 16 + lg;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -426,17 +426,11 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
           for (int i = 0; i < 4; ++i) {
             const float f = E ? hs[n][i & 1] * ks : hs[n][i & 1];
             s[k][n][i] = k < tiles && r0 + (i >> 1) * 8 < nb ? s[k][n][i] * f : -INFINITY;
-            mx[n][i & 1] = fmaxf(mx[n][i & 1], s[k][n][i]);
+            mx[n][i & 1] = fmaxf(mx[n][i & 1], E ? s[k][n][i] + lv[k] : s[k][n][i]);
           }
         }
       }
-      float vnew = vref;
-      if (E) {
-#pragma unroll
-        for (int k = 0; k < C::kTT; ++k) vnew = fmaxf(vnew, vs[k]);
-      }
-      const float beta = E ? vref / vnew : 1.f;
-      bool same = beta == 1.f;
+      bool same = true;
       float alpha[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -455,34 +449,35 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
       if (!__all_sync(0xffffffffu, same)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float f0 = alpha[n][0] * beta, f1 = alpha[n][1] * beta;
 #pragma unroll
           for (int c = 0; c < DH / 16; ++c) {
-            o[c][n][0] *= f0;
-            o[c][n][1] *= f1;
-            o[c][n][2] *= f0;
-            o[c][n][3] *= f1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[c][n][i] *= alpha[n][i & 1];
           }
         }
       }
-      vref = vnew;
 #pragma unroll
       for (int k = 0; k < C::kTT; ++k) {
         if (k >= tiles) break;
         uint32_t ph[NT][2], pl[NT][2];
-        const float vr = E ? vs[k] / vref : 1.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float e[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float mm = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1];
-            e[i] = ex2(s[k][n][i] - mm);
-            l[n][i & 1] += e[i];
+          for (int i = 0; i < 2; ++i) {
+            const float mm = m[n][i] == -INFINITY ? 0.f : m[n][i];
+            float add = lv[k] - mm;
+            if (E) {  // weights below 2^-60 are zero in f16; raised, their fp32 sum does not underflow
+              const float top = fmaxf(s[k][n][i], s[k][n][i + 2]);
+              if (top != -INFINITY && add < -60.f - top) add = -60.f - top;  // a NaN scale stays
+            }
+            e[i] = ex2(s[k][n][i] + add);
+            e[i + 2] = ex2(s[k][n][i + 2] + add);
+            l[n][i] += E ? (e[i] + e[i + 2]) * ex2(-mm - add) : e[i] + e[i + 2];
           }
           if (E) {
-            ph[n][0] = movmatrix(pack_f16x2(e[0] * vr, e[1] * vr));
-            ph[n][1] = movmatrix(pack_f16x2(e[2] * vr, e[3] * vr));
+            ph[n][0] = movmatrix(pack_f16x2(e[0], e[1]));
+            ph[n][1] = movmatrix(pack_f16x2(e[2], e[3]));
           } else {
             const uint32_t h0 = pack_bf16x2(e[0], e[1]), h1 = pack_bf16x2(e[2], e[3]);
             ph[n][0] = movmatrix(h0);
@@ -534,7 +529,6 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
         if (bad) l[n][i] = -1.f;
       }
     if (bad && lane == 0) atomicOr(p.status, SLIM_DEV_BADPAGE);
-    const float unit = E ? vref : 1.f;
     const bool whole = sg.tile == 0 && sg.end == sg.T;
     const bool last = cur.left <= 0;
     if (whole) {
@@ -544,7 +538,7 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
         for (int i = 0; i < 4; ++i) {
           const int hd = n * 8 + 2 * lq + (i & 1);
           if (hd >= nh) continue;
-          const float f = l[n][i & 1] > 0.f || l[n][i & 1] != l[n][i & 1] ? unit / l[n][i & 1] : 0.f;
+          const float f = l[n][i & 1] > 0.f || l[n][i & 1] != l[n][i & 1] ? 1.f / l[n][i & 1] : 0.f;
           __nv_bfloat16* dst = p.out + (static_cast<int64_t>(sg.b) * p.Hq + head0 + hd) * DH;
 #pragma unroll
           for (int c = 0; c < DH / 16; ++c) {
@@ -570,7 +564,7 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
 #pragma unroll
           for (int c = 0; c < DH / 16; ++c) {
             const int col = 16 * c + (E ? 2 * lg + (i >> 1) : lg + (i >> 1) * 8);
-            po[hd * DH + col] = o[c][n][i] * unit;
+            po[hd * DH + col] = o[c][n][i];
           }
           if (lg == 0 && i < 2) {
             pm[hd * 2] = m[n][i];

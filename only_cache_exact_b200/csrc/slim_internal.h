@@ -122,6 +122,12 @@ cudaError_t launch_paged_decode(const slim_paged_cache& c, const void* q, int64_
                                 int rows_extra, int Hq, int64_t t_hint, void* out, void* workspace, int32_t* status,
                                 cudaStream_t st, int* launches);
 
+bool paged_prefill_fits(const slim_paged_cache& c, int Hq, int64_t rows, int64_t max_new, int64_t t_hint);
+size_t paged_prefill_ws_bytes(const slim_paged_cache& c, int Hq, int64_t rows, int64_t max_new, int64_t t_hint);
+cudaError_t launch_paged_prefill(const slim_paged_cache& c, const void* q, int64_t q_stride, const int32_t* starts,
+                                 const int32_t* lens, int64_t rows, int64_t max_new, int Hq, int64_t t_hint,
+                                 void* out, void* workspace, int32_t* status, cudaStream_t st, int* launches);
+
 // Step front end: q = x·W_Q (fp32) and, with W_K, k = x·W_K (cache dtype) for B input rows.
 bool front_tc_supported(int dtype, int d);
 int front_tc_split(int d, bool with_k);  // cluster size of the tcgen05 front end

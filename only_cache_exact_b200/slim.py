@@ -32,7 +32,7 @@ EXPORTS = [
     "slim_prefill_attention_workspace_bytes", "slim_prefill_attention", "slim_project_qk",
     "slim_decode_step_x_workspace_bytes", "slim_decode_step_x", "slim_noalloc_scratch_bytes",
     "slim_mha_paged_append", "slim_mha_paged_gather", "slim_mha_paged_decode_workspace_bytes",
-    "slim_mha_paged_decode",
+    "slim_mha_paged_decode", "slim_mha_paged_prefill_workspace_bytes", "slim_mha_paged_prefill",
 ]
 
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -71,6 +71,8 @@ _SIGS = {
                                      _i64, _i32, _vp, _vp, _vp]),
     "slim_mha_paged_gather": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     "slim_mha_paged_decode_workspace_bytes": (_sz, [_vp, _i32]),
+    "slim_mha_paged_prefill_workspace_bytes": (_sz, [_vp, _i32, _i64, _i64, _i64]),
+    "slim_mha_paged_prefill": (_i32, [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _i64, _vp, _vp, _sz, _vp, _vp]),
     "slim_mha_paged_decode": (_i32, [_vp, _vp, _i64, _vp, _i32, _i32, _i64, _vp, _vp, _sz, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -424,6 +426,34 @@ def slim_mha_paged_decode(cache: PagedKV, q: torch.Tensor, lens: torch.Tensor, o
         raise ValueError("q must have one row per sequence")
     _paged_call(_lib.slim_mha_paged_decode, "slim_mha_paged_decode", dev, stream, cache._ref, qp, qs,
                 _on_device(lens, "lens", dev, torch.int32, (cache.B,)), rows_extra, q.shape[1], t_hint,
+                _on_device(out, "out", dev, torch.bfloat16, q.shape),
+                _on_device(workspace, "workspace", dev, torch.uint8), workspace.numel(),
+                _on_device(status, "status", dev, torch.int32))
+
+
+def slim_mha_paged_prefill_workspace_bytes(cache: PagedKV, Hq: int, rows: int, max_new: int = 0,
+                                           t_hint: int = 0) -> int:
+    with torch.cuda.device(cache.device):
+        return int(_lib.slim_mha_paged_prefill_workspace_bytes(cache._ref, Hq, rows, max_new, t_hint))
+
+
+def alloc_paged_prefill_workspace(cache: PagedKV, Hq: int, rows: int, max_new: int = 0,
+                                  t_hint: int = 0) -> torch.Tensor:
+    """Caller-owned scratch for slim_mha_paged_prefill with the same rows, max_new and t_hint (may be empty)."""
+    n = slim_mha_paged_prefill_workspace_bytes(cache, Hq, rows, max_new, t_hint)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def slim_mha_paged_prefill(cache: PagedKV, q: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor,
+                           out: torch.Tensor, workspace: torch.Tensor, status: torch.Tensor, max_new: int = 0,
+                           t_hint: int = 0, stream=None) -> None:
+    """Causal attention of the packed query rows q [rows][Hq][dh] bfloat16, row j of sequence b at position
+    lens[b] + j, over the paged cache; out [rows][Hq][dh] bfloat16."""
+    dev, rows = cache.device, q.shape[0]
+    qp, qs = _packed_rows(q, "q", dev, None, cache.dh)
+    _paged_call(_lib.slim_mha_paged_prefill, "slim_mha_paged_prefill", dev, stream, cache._ref, qp, qs,
+                _on_device(starts, "starts", dev, torch.int32, (cache.B + 1,)),
+                _on_device(lens, "lens", dev, torch.int32, (cache.B,)), rows, max_new, q.shape[1], t_hint,
                 _on_device(out, "out", dev, torch.bfloat16, q.shape),
                 _on_device(workspace, "workspace", dev, torch.uint8), workspace.numel(),
                 _on_device(status, "status", dev, torch.int32))

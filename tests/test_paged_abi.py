@@ -60,8 +60,16 @@ def decode(S, c=None, **kw):
                                              a["Hq"], a["hint"], a["out"], a["ws"], a["wsb"], a["status"], None)
 
 
+def prefill(S, c=None, **kw):
+    a = dict(q=F, qs=4096, starts=F, lens=F, rows=7, max_new=0, Hq=32, hint=0, out=F, ws=F, wsb=1 << 40, status=F)
+    a.update(kw)
+    return S.raw_lib().slim_mha_paged_prefill(cache(S) if c is None else c, a["q"], a["qs"], a["starts"], a["lens"],
+                                              a["rows"], a["max_new"], a["Hq"], a["hint"], a["out"], a["ws"], a["wsb"],
+                                              a["status"], None)
+
+
 @pytest.mark.parametrize("kw,code", BAD_CACHES)
-@pytest.mark.parametrize("call", [append, gather, decode])
+@pytest.mark.parametrize("call", [append, gather, decode, prefill])
 def test_cache_refusals(S, call, kw, code):
     assert call(S, cache(S, **kw)) == getattr(S, "SLIM_" + code)
     assert S.raw_lib().slim_mha_paged_decode_workspace_bytes(cache(S, **kw), 32) == 0
@@ -69,7 +77,7 @@ def test_cache_refusals(S, call, kw, code):
 
 def test_null_cache(S):
     null = ctypes.POINTER(S._PagedCacheC)()
-    for call in (append, gather, decode):
+    for call in (append, gather, decode, prefill):
         assert call(S, null) == S.SLIM_EINVAL
 
 
@@ -100,9 +108,31 @@ def test_decode_refusals(S, kw, code):
     assert decode(S, **kw) == getattr(S, "SLIM_" + code)
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), "EINVAL"), (dict(lens=None), "EINVAL"), (dict(starts=None), "EINVAL"), (dict(out=None), "EINVAL"),
+    (dict(status=None), "EINVAL"), (dict(q=F + 8), "EINVAL"), (dict(out=F + 2), "EINVAL"), (dict(qs=4000), "EINVAL"),
+    (dict(rows=-1), "EINVAL"), (dict(max_new=-2), "EINVAL"), (dict(Hq=12), "EINVAL"), (dict(rows=1 << 31), "EINVAL"),
+    (dict(Hq=8 * 129, qs=1 << 20), "EUNSUPPORTED"), (dict(ws=None), "EWORKSPACE"), (dict(ws=F + 16), "EWORKSPACE"),
+    (dict(wsb=100), "EWORKSPACE"),
+])
+def test_prefill_refusals(S, kw, code):
+    # 7 rows of 4 sequences over a capacity of 1280 rows: too few CTAs, so keys are split and need scratch
+    assert S.raw_lib().slim_mha_paged_prefill_workspace_bytes(cache(S), 32, 7, 0, 0) > 100
+    assert prefill(S, **kw) == getattr(S, "SLIM_" + code)
+
+
+def test_prefill_workspace(S):
+    size = S.raw_lib().slim_mha_paged_prefill_workspace_bytes
+    assert size(cache(S), 32, 7, 0, 128) == 0       # short: one CTA walks all keys
+    assert size(cache(S), 32, 8000, 0, 0) == 0      # many rows: CTAs enough
+    assert size(cache(S), 31, 7, 0, 0) == 0 and size(cache(S), 32, 0, 0, 0) == 0
+    assert size(cache(S), 32, 7, 0, 1 << 40) == size(cache(S), 32, 7, 0, 0)  # a hint past the capacity is the capacity
+
+
 def test_nothing_to_do(S):
     assert append(S, rows=0, k=None, v=None, q=None, q_out=None) == S.SLIM_OK
     assert gather(S, rows=0, k=None, v=None) == S.SLIM_OK
+    assert prefill(S, rows=0, q=None, out=None, ws=None) == S.SLIM_OK
     assert S.slim_last_launch_count() == 0
 
 

@@ -1,0 +1,254 @@
+"""slim_mha_paged_prefill against the float64 oracle.
+
+Tolerance, element by element, with o the output, A = Σ p|V| and D the largest Σ_c |q_c K_tc|/sqrt(dh):
+  output rounded to bf16           2^-8 |o|
+  scores: dh products summed in fp32, then roundings of the factors and the base-2 exponential (2^-22):
+          |δs| <= (dh + 8)·2^-24·D, and p, also through the sum in the denominator, moves by 2 δs
+  probabilities rounded for the MMA: 2^-8 for bf16 values, 2^-11 (f16) for e4m3
+  sums in fp32, joins of splits, f16 underflow: 2^-16 A
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as P
+from tests.paged_cases import PagedState, angles, f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def S():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from only_cache_exact_b200 import slim
+    return slim
+
+
+def bound(kind, dh, o, A, D):
+    ds = (dh + 8) * 2.0 ** -24 * D + 2.0 ** -22
+    return 2.0 ** -8 * np.abs(o) + A * (2 * ds + (2.0 ** -11 if kind == "e4m3" else 2.0 ** -8) + 2.0 ** -16)
+
+
+def run(S, st, q, n, cached, max_new=0, t_hint=0, first=0, out=None, lens=None):
+    Hq = q.shape[1]
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda") if out is None else out
+    ws = S.alloc_paged_prefill_workspace(st.cache, Hq, q.shape[0], max_new, t_hint)
+    ws.fill_(0xFF)
+    S.slim_mha_paged_prefill(st.cache, q, st.starts(n, first), st.lens if lens is None else lens, out, ws, st.status,
+                             max_new=max_new, t_hint=t_hint)
+    torch.cuda.synchronize()
+    return out
+
+
+def check(st, q, out, n, cached, first=0):
+    r = first
+    for b, (a, k) in enumerate(zip(cached, n)):
+        if k:
+            K, V = (st.oracle[w].read(st.table_h[b], a + k) for w in (0, 1))
+            o, A, D = P.attend(f64(q[r:r + k]), K, V, [a + j for j in range(k)])
+            err = np.abs(f64(out[r:r + k]) - o)
+            lim = bound(st.kind, st.dh, o, A, D)
+            assert (err <= lim).all(), (b, a, k, (err / lim).max(), np.argwhere(err > lim)[0].tolist())
+        r += k
+
+
+CASES = [
+    # Hq, Hkv, dh, page, cached, new
+    (4, 4, 64, 16, [0], [1]),
+    (4, 4, 64, 16, [0, 0, 0], [16, 130, 1]),
+    (2, 2, 128, 64, [0, 63, 64], [129, 65, 64]),
+    (6, 2, 64, 32, [100, 0, 31, 5], [3, 85, 0, 200]),       # 42 queries a tile, rows left over
+    (7, 1, 128, 128, [300, 1], [40, 128]),
+    (16, 1, 128, 16, [0, 511, 512], [9, 1, 17]),
+    (64, 1, 64, 64, [700], [5]),                            # 2 queries a tile
+    (128, 1, 128, 32, [33, 0], [2, 3]),                     # 1 query a tile
+    (5, 5, 64, 128, [127, 128, 129], [1, 1, 1]),
+    (3, 1, 128, 16, [0], [700]),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,dh,page,cached,new", CASES)
+@pytest.mark.parametrize("t_hint", [1, 0])
+def test_ragged(S, kind, Hq, Hkv, dh, page, cached, new, t_hint):
+    """Odd sizes, grouped heads and chunks; t_hint = 1 keeps each tile's keys in one CTA, 0 may split them."""
+    st = PagedState(S, kind, Hkv, dh, page, [a + n for a, n in zip(cached, new)], [a + n for a, n in zip(cached, new)],
+                    seed=21)
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    big = st.rows(new, Hq + 2, 2.0)  # queries as a slice: rows lie apart
+    pad = torch.zeros(3, Hq + 2, dh, dtype=torch.bfloat16, device="cuda")
+    q = torch.cat([pad[:1], big, pad])[:, 1:1 + Hq]
+    out = run(S, st, q, new, cached, max_new=max(new) if t_hint else 0, t_hint=t_hint, first=1)
+    assert int(st.status.item()) == 0
+    total = sum(new)
+    assert (out[0] == 7).all() and (out[1 + total:] == 7).all()  # rows of no sequence stay as they were
+    check(st, q, out, new, cached, first=1)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dh,page,G", [(64, 16, 1), (128, 64, 4), (128, 128, 8)])
+def test_long_cache_few_rows(S, kind, dh, page, G):
+    """Keys split over many CTAs and joined, among them splits that a short sequence has nothing in."""
+    cached, new = [5000, 3, 2047], [3, 2, 1]
+    st = PagedState(S, kind, 1, dh, page, [a + n for a, n in zip(cached, new)], [a + n for a, n in zip(cached, new)],
+                    seed=22)
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows(new, G, 2.0)
+    out = run(S, st, q, new, cached, max_new=3)
+    assert S.slim_last_launch_count() == 2 and int(st.status.item()) == 0
+    check(st, q, out, new, cached)
+    assert torch.equal(out, run(S, st, q, new, cached, max_new=3))
+    one = run(S, st, q, new, cached, max_new=3, t_hint=1)  # unsplit
+    assert S.slim_last_launch_count() == 1
+    check(st, q, one, new, cached)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_agrees_with_decode(S, kind):
+    """One new row per sequence: the two forms of the attention agree within their tolerances."""
+    cached = [0, 100, 1500]
+    st = PagedState(S, kind, 4, 128, 32, [c + 1 for c in cached], [c + 1 for c in cached], seed=23)
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows([1, 1, 1], 8, 2.0)
+    a = run(S, st, q, [1, 1, 1], cached, max_new=1)
+    b = torch.empty_like(a)
+    S.slim_mha_paged_decode(st.cache, q, st.lens, b, S.alloc_paged_decode_workspace(st.cache, 8), st.status)
+    torch.cuda.synchronize()
+    check(st, q, a, [1, 1, 1], cached)
+    check(st, q, b, [1, 1, 1], cached)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("t_hint", [1, 0])
+def test_skipped_sequences(S, kind, t_hint):
+    """Bad lengths give zero rows; a page outside the pool gives zeros to the rows that reach it and only to them."""
+    cached, new = [3, 9, 40, 700], [4, 4, 30, 6]
+    st = PagedState(S, kind, 2, 64, 16, [a + n for a, n in zip(cached, new)], [a + n for a, n in zip(cached, new)],
+                    seed=24)
+    cap = st.cache.cap
+    st.table[2, 3] = -1      # positions 48..63
+    st.table[3, 7] = 1 << 30
+    lens = torch.tensor([-1, cap - 2, 40, 700], dtype=torch.int32, device="cuda")
+    q = st.rows(new, 4)
+    out = run(S, st, q, new, cached, max_new=30, t_hint=t_hint, lens=lens)
+    assert int(st.status.item()) == S.SLIM_DEV_BADLEN | S.SLIM_DEV_OVERFLOW | S.SLIM_DEV_BADPAGE
+    assert (out[:8] == 0).all() and (out[16:] == 0).all()
+    K, V = (st.oracle[w].read(st.table_h[2], 48) for w in (0, 1))
+    o, A, D = P.attend(f64(q[8:16]), K, V, list(range(40, 48)))
+    assert (np.abs(f64(out[8:16]) - o) <= bound(kind, 64, o, A, D)).all()
+    st.status.zero_()
+    bad = torch.tensor([0, 4, 2, 38, 50], dtype=torch.int32, device="cuda")  # descending, then past the rows
+    ws = S.alloc_paged_prefill_workspace(st.cache, 4, q.shape[0], 44, t_hint)
+    S.slim_mha_paged_prefill(st.cache, q, bad, st.lens, out, ws, st.status, max_new=44, t_hint=t_hint)
+    torch.cuda.synchronize()
+    assert int(st.status.item()) & S.SLIM_DEV_BADLEN
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("t_hint", [1, 0])
+def test_large_scores_and_scales(S, kind, t_hint):
+    """Scores far beyond the exponential's range, growing maxima (late keys dominate), pages whose value scales lie
+    2^40 apart, zero queries."""
+    st = PagedState(S, kind, 1, 64, 16, [600], [600], seed=25)
+    pid = [int(x) for x in st.table_h[0, :38]]
+    for i, p in enumerate(pid):
+        fk = 2.0 ** (i // 6)
+        fv = 2.0 ** 20 if i == 9 else 2.0 ** -20 if i == 20 else 1.0
+        for w, f in ((0, fk), (1, fv)):
+            if kind == "e4m3":
+                st.scales[w][p] *= f
+                st.oracle[w].scale[p] *= f
+            else:
+                st.pages[w][p] *= f
+            st.oracle[w].values[p] *= f
+    n, cached = [300], [300]
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows(n, 3, 10.0)
+    q[5, 1] = 0
+    out = run(S, st, q, n, cached, max_new=300, t_hint=t_hint)
+    check(st, q, out, n, cached)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_chunks_then_tokens(S, kind):
+    """A prompt in chunks, each appended and attended, then single tokens: a model layer's use of the cache, captured
+    per chunk size and on a stream of its own."""
+    Hq, Hkv, dh, page = 8, 2, 64, 16
+    st = PagedState(S, kind, Hkv, dh, page, [0, 0], [160, 120], seed=26)
+    cos, sin = angles(st.cache.cap, dh)
+    cached = [0, 0]
+    ws1 = S.alloc_paged_decode_workspace(st.cache, Hq)
+    s = torch.cuda.Stream()
+    for n in ([100, 37], [20, 60], [1, 1], [3, 0], [1, 1]):
+        k, v, q = st.rows(n, Hkv), st.rows(n, Hkv), st.rows(n, Hq, 2.0)
+        qr, out = torch.empty_like(q), torch.empty_like(q)
+        starts = st.starts(n)
+        ws = S.alloc_paged_prefill_workspace(st.cache, Hq, sum(n), max(n))
+        s.wait_stream(torch.cuda.current_stream())
+        S.slim_mha_paged_append(st.cache, k, v, starts, st.lens, st.status, q=q, q_out=qr, cos=cos, sin=sin,
+                                max_new=max(n), stream=s)
+        if n == [1, 1]:
+            S.slim_mha_paged_decode(st.cache, qr, st.lens, out, ws1, st.status, stream=s)
+        else:
+            S.slim_mha_paged_prefill(st.cache, qr, starts, st.lens, out, ws, st.status, max_new=max(n), stream=s)
+        s.synchronize()
+        for w in (0, 1):
+            st.oracle[w].values = np.nan_to_num(st.values(w), nan=0.0)
+        check(st, qr, out, n, cached)
+        cached = [a + b for a, b in zip(cached, n)]
+        st.lens += torch.tensor(n, dtype=torch.int32, device="cuda")
+    assert int(st.status.item()) == 0
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("t_hint", [1, 0])
+def test_poisoned_page(S, which, t_hint):
+    """A page whose scale is NaN makes the outputs that attend a row of it NaN, in both forms, and no other."""
+    st = PagedState(S, "e4m3", 1, 64, 16, [700], [700], seed=29)
+    st.lens = torch.tensor([600], dtype=torch.int32, device="cuda")
+    x = st.rows([20], 1)
+    x[16] = float("inf")  # row 656
+    ok = st.rows([20], 1)
+    k, v = (x, ok) if which == 0 else (ok, x)
+    S.slim_mha_paged_append(st.cache, k, v, st.starts([20]), st.lens + 40, st.status)
+    torch.cuda.synchronize()
+    for w in (0, 1):
+        st.oracle[w].values = np.nan_to_num(st.values(w), nan=0.0)
+    q = st.rows([100], 4)
+    out = run(S, st, q, [100], [600], max_new=100, t_hint=t_hint)
+    # row 656 begins a page: rows 656..671 share its scale
+    assert torch.isnan(out[56:]).all() and torch.isfinite(out[:56]).all()
+    check(st, q[:56], out[:56], [56], [600])
+    for n, bad in ((655, False), (656, True)):
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        o = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+        S.slim_mha_paged_decode(st.cache, q[:1], lens, o, S.alloc_paged_decode_workspace(st.cache, 4), st.status,
+                                t_hint=t_hint)
+        assert torch.isnan(o).all().item() == bad and torch.isfinite(o).all().item() != bad
+    assert int(st.status.item()) == 0
+
+
+def test_capture(S):
+    st = PagedState(S, "e4m3", 2, 128, 32, [400, 150], [400, 150], seed=27)
+    n, cached = [100, 1], [300, 149]
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows(n, 4, 2.0)
+    want = run(S, st, q, n, cached, max_new=100)
+    out = torch.zeros_like(want)
+    ws = S.alloc_paged_prefill_workspace(st.cache, 4, 101, 100)
+    starts = st.starts(n)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        S.slim_mha_paged_prefill(st.cache, q, starts, st.lens, out, ws, st.status, max_new=100)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_no_rows(S):
+    st = PagedState(S, "bf16", 2, 64, 16, [9, 0], [40, 40], seed=28)
+    e = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    S.slim_mha_paged_prefill(st.cache, e, st.starts([0, 0]), st.lens, e,
+                             torch.empty(0, dtype=torch.uint8, device="cuda"), st.status)
+    assert S.slim_last_launch_count() == 0
