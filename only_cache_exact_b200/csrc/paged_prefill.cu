@@ -9,22 +9,21 @@
 // head) pair, the G query heads that share the key head side by side, so that a
 // tile holds 128/G queries and every K and V tile it loads serves all of them.
 // It walks the 128-key tiles up to its last query's position.
-//   warp 0        loads K and V, page by page: bf16 by TMA straight into the MMA's
-//                 128-byte swizzle (rings of 2 (dh = 128) or 4 tiles); e4m3 by bulk
-//                 copies of whole page heads into one raw K and one raw V tile
+//   warp 0        loads K and V, page by page, by TMA straight into the MMAs' swizzled layouts;
+//                 e4m3 values as bulk copies of whole page heads into a raw ring
 //   warp 1        issues tcgen05.mma: S_t = Q_t·K^T into the tile's TMEM S region,
 //                 O_t += P_t·V with P_t read from tensor memory, in the order
 //                 P_0(j)·V_j, S_0(j+1), P_1(j)·V_j, S_1(j+1)
 //   warps 4..7, 8..11  softmax of tile 0 and 1, one row per thread: causal mask,
 //                 lazy running maximum (O is rescaled only when a maximum grows by
 //                 more than 2^8), P over the S region, row sums in fp32
-//   warps 12..15  (e4m3) codes to f16 in the MMA's layout
-// e4m3 codes are exact in f16, so the MMAs of an e4m3 cache run in f16 on the bare
-// codes: the key scale of a page multiplies its scores, the value scale 2^lv its
-// probabilities, P = 2^(s + lv - m) with m the running maximum of s + lv, and
-// the query is brought into f16's range by a power of two per row. P is rounded
-// to f16 (2^-11) there; over bf16 values it is rounded to bf16 (2^-8), the type
-// the MMA wants beside them.
+//   warps 12..15  (e4m3) value codes to f16 in the MMA's layout
+// An e4m3 cache is used as it is stored. S runs in e4m3 on the key codes, with the query in two
+// e4m3 parts (high and low) that together hold a bf16 exactly: twice the products at twice the
+// rate of f16, and no key is converted. Value codes are exact in f16, and P·V runs in f16. The
+// key scale of a page multiplies its scores, the value scale 2^lv its probabilities,
+// P = 2^(s + lv - m) with m the running maximum of s + lv. P is rounded to f16 (2^-11) there;
+// over bf16 values it is rounded to bf16 (2^-8), the type the MMA wants beside them.
 // Key rows at or past the sequence's end are zeroed in V before the first MMA
 // that reads them: a masked P = 0 never meets what a page held before.
 //
@@ -43,6 +42,7 @@ constexpr int kFQ = 128;  // rows of a tile
 constexpr int kFK = 128;  // keys of a tile
 constexpr uint32_t kFTmemPerTile = 256;  // S (and P over it) at columns 0..127, O at 128
 constexpr float kFLazyLog2 = 8.f;
+constexpr int kFPart1 = 96;  // keys of P that are handed over first
 
 struct PagedPrefillParams {
   PagedView c;
@@ -52,6 +52,7 @@ struct PagedPrefillParams {
   const int32_t* lens;
   int64_t rows, max_new;
   int Hq, G, QPT;  // QPT = 128 / G queries of a tile
+  uint32_t g_inv;  // ceil(2^16 / G): row / G = row * g_inv >> 16 for row < 128
   int pairs, splits;
   __nv_bfloat16* out;
   float* ws_o;   // [split][rows][Hq][dh], splits > 1
@@ -63,11 +64,14 @@ struct PagedPrefillParams {
 template <bool E, int DHB>
 struct PfCfg {
   static constexpr int DH = 64 * DHB;
-  static constexpr int NS = DHB == 2 ? 2 : 4;                  // tiles of a K and a V ring
-  static constexpr uint32_t kTile = kFK * DH * 2u;             // bytes of a 16-bit K, V or Q tile
-  static constexpr uint32_t kRaw = E ? kFK * DH : 0u;          // bytes of a raw e4m3 tile
+  static constexpr int NK = E ? 3 : DHB == 2 ? 2 : 4;          // stages of the K ring
+  static constexpr int NV = DHB == 2 ? 2 : 4;                  // stages of the V ring the MMAs read
+  static constexpr int NR = 2;                                 // stages of the raw V ring (e4m3)
+  static constexpr uint32_t kTile = kFK * DH * 2u;             // bytes of a 16-bit V tile, of a Q tile (16-bit, or e4m3 twice)
+  static constexpr uint32_t kKTile = E ? kFK * DH : kTile;     // bytes of a K tile
+  static constexpr uint32_t kRaw = E ? kFK * DH : 0u;          // bytes of a raw V tile
   static constexpr int kThreads = E ? 512 : 384;
-  static constexpr uint32_t kSmem = 2u * kTile + 2u * NS * kTile + 2u * kRaw + 512u + 1024u;
+  static constexpr uint32_t kSmem = 2u * kTile + NK * kKTile + NV * kTile + NR * kRaw + 512u + 1024u;
 };
 
 __device__ __forceinline__ float pf_ex2(float x) {
@@ -92,9 +96,42 @@ __device__ __forceinline__ void pf_umma_tmem_a(uint32_t d_tmem, uint32_t a_tmem,
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// kind::f16 instruction descriptor with f16 A and B, fp32 D (both type fields 0).
-__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
+// D (TMEM) (+)= A · B, e4m3 operands from shared memory, 32 columns of the contraction.
+__device__ __forceinline__ void pf_umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor with both operand type fields 0 (f16 for kind::f16, e4m3 for kind::f8f6f4), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_zero_f32(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
   return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+constexpr uint32_t kLayoutSW64 = 4;  // 64-byte swizzle in a shared-memory descriptor
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// mbar_wait by a whole warp, one decision for it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 template <int N>
 __device__ __forceinline__ void reg_inc() {
@@ -110,30 +147,28 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const PagedPrefillParams p) {
   using C = PfCfg<E, DHB>;
-  constexpr int DH = C::DH, NS = C::NS;
-  constexpr uint32_t T = C::kTile;
+  constexpr int DH = C::DH, NK = C::NK, NV = C::NV, NR = C::NR;
+  constexpr uint32_t T = C::kTile, TK = C::kKTile;
   extern __shared__ uint8_t pf_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qs = sm;              // [row tile][DHB boxes][128 rows][128 B]
-  uint8_t* ks = qs + 2 * T;      // [stage][DHB boxes][128 rows][128 B]
-  uint8_t* vs = ks + NS * T;
-  uint8_t* rk = vs + NS * T;     // raw K, raw V tile (e4m3)
-  uint8_t* rv = rk + C::kRaw;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(rv + C::kRaw);
+  uint8_t* qs = sm;              // bf16: [row tile][DHB boxes][128 rows][128 B]; e4m3: [row tile][high, low][128 rows][DH]
+  uint8_t* ks = qs + 2 * T;      // [stage] bf16: [DHB boxes][128 rows][128 B]; e4m3: [128 rows][DH]
+  uint8_t* vs = ks + NK * TK;    // [stage][DHB boxes][128 rows][128 B]
+  uint8_t* rv = vs + NV * T;     // [stage][128 rows][DH] raw V (e4m3)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rv + NR * C::kRaw);
   uint64_t* qbar = bars;           // Q written by the softmax warps
-  uint64_t* kfull = bars + 1;      // [NS]
-  uint64_t* kempty = kfull + NS;   // [NS]
-  uint64_t* vfull = kempty + NS;   // [NS]
-  uint64_t* vempty = vfull + NS;   // [NS]
-  uint64_t* sfull = vempty + NS;   // [2] S written
-  uint64_t* pready = sfull + 2;    // [2] P written over S (and O rescaled)
-  uint64_t* pfree = pready + 2;    // [2] the P·V MMA completed
-  uint64_t* ofull = pfree + 2;     // [2] the tile's last P·V MMA completed
-  uint64_t* rfull = ofull + 2;     // [2] raw K, raw V landed
-  uint64_t* rempty = rfull + 2;    // [2] raw K, raw V converted
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rempty + 2);
+  uint64_t* kfull = bars + 1;      // [NK]
+  uint64_t* kempty = kfull + NK;   // [NK]
+  uint64_t* vfull = kempty + NK;   // [NV]
+  uint64_t* vempty = vfull + NV;   // [NV]
+  uint64_t* sfull = vempty + NV;   // [2] S written
+  uint64_t* pready = sfull + 2;    // [part][2] P of the part's keys written over S (and O rescaled)
+  uint64_t* ofull = pready + 4;    // [2] the tile's last P·V MMA completed
+  uint64_t* rfull = ofull + 2;     // [NR] raw V landed
+  uint64_t* rempty = rfull + NR;   // [NR] raw V converted
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rempty + NR);
   int* s_bad = reinterpret_cast<int*>(tmem_slot + 1);  // first position whose page is outside the pool
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   pdl_launch_dependents();
   pdl_wait_primary();
@@ -170,19 +205,23 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
 
   if (warp == 0 && lane == 0) {
     mbar_init(qbar, 8);
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&kfull[s], E ? 4 : 1);
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], 1);
+    }
+    for (int s = 0; s < NV; ++s) {
       mbar_init(&vfull[s], E ? 4 : 1);
       mbar_init(&vempty[s], 1);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(&rfull[s], 1);
+      mbar_init(&rempty[s], 4);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
       mbar_init(&pready[t], 4);
-      mbar_init(&pfree[t], 1);
+      mbar_init(&pready[2 + t], 4);
       mbar_init(&ofull[t], 1);
-      mbar_init(&rfull[t], 1);
-      mbar_init(&rempty[t], 4);
     }
     *s_bad = 0x7fffffff;
     fence_barrier_init();
@@ -193,15 +232,18 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
   const int psh = p.c.page_shift, ppt = kFK >> psh;  // pages of a key tile
   const int page_lo = kt0 * ppt, page_hi = min(kt1 * ppt, ((L - 1) >> psh) + 1);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  int first_bad = 0x7fffffff;
   for (int i = page_lo + static_cast<int>(threadIdx.x); i < page_hi; i += C::kThreads) {
     const int id = __ldg(table + i);
-    if (id < 0 || id >= p.c.num_pages) atomicMin(s_bad, i << psh);
+    if (id < 0 || id >= p.c.num_pages) first_bad = min(first_bad, i << psh);
   }
-  __syncthreads();
+  tc_fence_before();
+  if (__syncthreads_or(first_bad != 0x7fffffff)) {
+    if (first_bad != 0x7fffffff) atomicMin(s_bad, first_bad);
+    __syncthreads();
+  }
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   // keys from here on are not used: the sequence's end, or a page outside the pool (whose place page 0
   // takes in the loads)
   const int Lz = min(L, *s_bad);
@@ -215,7 +257,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   auto pages_of = [&](int j) { return min(ppt, ((L - 1 - j * kFK) >> psh) + 1); };
 
   if (warp < 4) {
-    reg_dec<48>();
+    reg_dec<E ? 64 : 72>();
     if (warp == 0) {
       // ------------------------------------------------------------ loads
       int nk_issued = 0, nv_issued = 0;
@@ -224,170 +266,193 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         const int j = kt0 + i, npg = pages_of(j), id = id_next;
         if (i + 1 < nkt) id_next = lane < pages_of(j + 1) ? page_id((j + 1) * ppt + lane) : 0;
         const uint32_t bytes = static_cast<uint32_t>(npg << psh) * DH * (E ? 1u : 2u);
-        if (E) {
-          const uint32_t ph = static_cast<uint32_t>(i & 1);
-          const int64_t src = id * p.c.page_bytes + h * p.c.head_bytes;
-          const uint32_t hb = static_cast<uint32_t>(p.c.head_bytes);
-          if (i > 0 && !__all_sync(0xffffffffu, mbar_wait(&rempty[0], ph ^ 1u, p.status))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&rfull[0], bytes);
-          __syncwarp();
-          if (lane < npg) bulk_load_g2s(rk + lane * hb, p.c.k + src, hb, &rfull[0]);
-          ++nk_issued;
-          if (i > 0 && !__all_sync(0xffffffffu, mbar_wait(&rempty[1], ph ^ 1u, p.status))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&rfull[1], bytes);
-          __syncwarp();
-          if (lane < npg) bulk_load_g2s(rv + lane * hb, p.c.v + src, hb, &rfull[1]);
-          ++nv_issued;
-        } else {
-          const int s = i % NS;
-          const uint32_t ph = static_cast<uint32_t>((i / NS) & 1);
-          const int y = (id * p.c.Hkv + h) << psh;
-          const uint32_t off = static_cast<uint32_t>(lane << psh) * 128u;
-          if (i >= NS && !__all_sync(0xffffffffu, mbar_wait(&kempty[s], ph ^ 1u, p.status))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&kfull[s], bytes);
-          __syncwarp();
-          if (lane < npg) {
+        const int y = (id * p.c.Hkv + h) << psh;  // first line of the page's head
+        const uint32_t line = static_cast<uint32_t>(lane << psh);
+        const int sk = i % NK;
+        if (i >= NK && !warp_wait(&kempty[sk], static_cast<uint32_t>(i / NK - 1) & 1u, p.status)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&kfull[sk], bytes);
+        __syncwarp();
+        if (lane < npg) {
+          if (E) {
+            tma_load_2d(ks + sk * TK + line * DH, &kmap, 0, y, &kfull[sk], l2_policy_evict_last());
+          } else {
 #pragma unroll
             for (int k = 0; k < DHB; ++k)
-              tma_load_2d(ks + s * T + k * 16384 + off, &kmap, 64 * k, y, &kfull[s], l2_policy_evict_last());
+              tma_load_2d(ks + sk * TK + k * 16384 + line * 128u, &kmap, 64 * k, y, &kfull[sk], l2_policy_evict_last());
           }
-          ++nk_issued;
-          if (i >= NS && !__all_sync(0xffffffffu, mbar_wait(&vempty[s], ph ^ 1u, p.status))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&vfull[s], bytes);
-          __syncwarp();
-          if (lane < npg) {
-#pragma unroll
-            for (int k = 0; k < DHB; ++k)
-              tma_load_2d(vs + s * T + k * 16384 + off, &vmap, 64 * k, y, &vfull[s], l2_policy_evict_last());
-          }
-          ++nv_issued;
         }
+        ++nk_issued;
+        constexpr int N = E ? NR : NV;
+        const int sv = i % N;
+        uint64_t* full = E ? &rfull[sv] : &vfull[sv];
+        if (i >= N && !warp_wait(E ? &rempty[sv] : &vempty[sv], static_cast<uint32_t>(i / N - 1) & 1u, p.status)) break;
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        __syncwarp();
+        if (lane < npg) {
+          if (E) {
+            bulk_load_g2s(rv + sv * C::kRaw + line * DH, p.c.v + id * p.c.page_bytes + h * p.c.head_bytes,
+                          static_cast<uint32_t>(p.c.head_bytes), full);
+          } else {
+#pragma unroll
+            for (int k = 0; k < DHB; ++k)
+              tma_load_2d(vs + sv * T + k * 16384 + line * 128u, &vmap, 64 * k, y, full, l2_policy_evict_last());
+          }
+        }
+        ++nv_issued;
       }
       // every issued copy lands before the CTA exits
-      if (E) {
-        if (nk_issued > 0) mbar_wait(&rfull[0], static_cast<uint32_t>(nk_issued - 1) & 1u, p.status);
-        if (nv_issued > 0) mbar_wait(&rfull[1], static_cast<uint32_t>(nv_issued - 1) & 1u, p.status);
-      } else {
-        for (int u = max(0, nk_issued - NS); u < nk_issued; ++u)
-          mbar_wait(&kfull[u % NS], static_cast<uint32_t>(u / NS) & 1u, p.status);
-        for (int u = max(0, nv_issued - NS); u < nv_issued; ++u)
-          mbar_wait(&vfull[u % NS], static_cast<uint32_t>(u / NS) & 1u, p.status);
-      }
-    } else if (warp == 1 && lane == 0) {
+      constexpr int N = E ? NR : NV;
+      for (int u = max(0, nk_issued - NK); u < nk_issued; ++u)
+        mbar_wait(&kfull[u % NK], static_cast<uint32_t>(u / NK) & 1u, p.status);
+      for (int u = max(0, nv_issued - N); u < nv_issued; ++u)
+        mbar_wait(E ? &rfull[u % N] : &vfull[u % N], static_cast<uint32_t>(u / N) & 1u, p.status);
+    } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      const uint32_t idesc_s = E ? idesc_f16_f32(kFQ, kFK, 0u, 0u) : idesc_bf16_f32(kFQ, kFK, 0u, 0u);
-      const uint32_t idesc_o = E ? idesc_f16_f32(kFQ, DH, 0u, 1u) : idesc_bf16_f32(kFQ, DH, 0u, 1u);
-      const uint32_t qb = smem_u32(qs), kb0 = smem_u32(ks), vb0 = smem_u32(vs);
-      int nk[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) nk[t] = tile_end(t) - kt0;
-      bool ok = mbar_wait(qbar, 0u, p.status);
-      auto issue_s = [&](int t, int i) {
-        const int s = i % NS;
-        if (!mbar_wait(&kfull[s], static_cast<uint32_t>(i / NS) & 1u, p.status)) return false;
+      // The whole warp walks the loop and one elected lane issues, so that descriptors stay in uniform
+      // registers: issued from a branch on the lane number, an MMA took 96 cycles instead of its 64.
+      const uint32_t idesc_s = E ? idesc_zero_f32(kFQ, kFK, 0u, 0u) : idesc_bf16_f32(kFQ, kFK, 0u, 0u);
+      const uint32_t idesc_o = E ? idesc_zero_f32(kFQ, DH, 0u, 1u) : idesc_bf16_f32(kFQ, DH, 0u, 1u);
+      // e4m3 rows of 64 bytes use the 64-byte swizzle, all others the 128-byte one
+      constexpr uint32_t kLay = E && DH == 64 ? kLayoutSW64 : kLayoutSW128, kSbo = E && DH == 64 ? 512u : 1024u;
+      const uint64_t qdesc = smem_desc(smem_u32(qs), 16, kSbo, kLay);
+      const uint64_t kdesc = smem_desc(smem_u32(ks), 16, kSbo, kLay);
+      const uint64_t vdesc = smem_desc(smem_u32(vs), 16384, 1024, kLayoutSW128);
+      const int nk0 = tile_end(0) - kt0, nk1 = nkt;
+      const bool lead = elect_one();
+      bool ok = warp_wait(qbar, 0u, p.status);
+      // S_t(i) = Q_t·K_i^T; the caller has waited for K_i
+      auto issue_s = [&](int t, int s) {
         tc_fence_after();
-        const uint32_t kb = kb0 + s * T, qtb = qb + t * T;
+        if (lead) {
+          const uint64_t kd = kdesc + static_cast<uint32_t>(s) * (TK >> 4), qd = qdesc + static_cast<uint32_t>(t) * (T >> 4);
+          if (E) {
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384u + (kk & 3) * 32u;
-          umma_f16(tmem + t * kFTmemPerTile, smem_desc(qtb + off, 16, 1024, kLayoutSW128),
-                   smem_desc(kb + off, 16, 1024, kLayoutSW128), idesc_s, kk > 0 ? 1u : 0u);
-        }
-        umma_commit(&sfull[t]);
-        if (t == 1) umma_commit(&kempty[s]);
-        return true;
-      };
-      auto issue_pv = [&](int t, int i) {
-        const int s = i % NS;
-        if (!mbar_wait(&pready[t], static_cast<uint32_t>(i) & 1u, p.status) ||
-            !mbar_wait(&vfull[s], static_cast<uint32_t>(i / NS) & 1u, p.status))
-          return false;
-        tc_fence_after();
-        const uint32_t vb = vb0 + s * T, pt = tmem + t * kFTmemPerTile;
+            for (int kk = 0; kk < DH / 32; ++kk)  // high and low part of Q on the same K columns
 #pragma unroll
-        for (int kk = 0; kk < kFK / 16; ++kk) {
-          pf_umma_tmem_a(tmem + t * kFTmemPerTile + 128u, pt + static_cast<uint32_t>(kk * 8),
-                         smem_desc(vb + kk * 2048u, 16384, 1024, kLayoutSW128), idesc_o,
-                         (i > 0 || kk > 0) ? 1u : 0u);
-        }
-        umma_commit(&pfree[t]);
-        if (t == 1) umma_commit(&vempty[s]);
-        return true;
-      };
-      bool committed[2];
+              for (int part = 0; part < 2; ++part)
+                pf_umma_f8(tmem + t * kFTmemPerTile, qd + part * (T >> 5) + kk * 2u, kd + kk * 2u, idesc_s,
+                           kk + part > 0 ? 1u : 0u);
+          } else {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        committed[t] = false;
-        if (ok && nk[t] > 0) ok = issue_s(t, 0);
-      }
-      for (int i = 0; ok && i < nk[1]; ++i) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || i >= nk[t]) continue;
-          if (!issue_pv(t, i)) ok = false;
-          if (ok && i == nk[t] - 1) {
-            umma_commit(&ofull[t]);
-            committed[t] = true;
+            for (int kk = 0; kk < DH / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
+              umma_f16(tmem + t * kFTmemPerTile, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+            }
           }
-          // S_t(i+1) overwrites the P that the P·V above reads: issued after it
-          if (ok && i + 1 < nk[t] && !issue_s(t, i + 1)) ok = false;
+          umma_commit(&sfull[t]);
+          if (t == 1) umma_commit(&kempty[s]);
+        }
+      };
+      // O_t += P_t(i)·V_i, in two parts: the first kFPart1 keys start while the softmax works on the rest
+      auto issue_pv = [&](int t, int i, int s) {
+        const uint32_t par = static_cast<uint32_t>(i) & 1u, pt = tmem + t * kFTmemPerTile;
+        const uint64_t vd = vdesc + static_cast<uint32_t>(s) * (T >> 4);
+        if (!warp_wait(&pready[t], par, p.status)) return false;
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int kk = 0; kk < kFPart1 / 16; ++kk)
+            pf_umma_tmem_a(pt + 128u, pt + static_cast<uint32_t>(kk * 8), vd + static_cast<uint32_t>(kk * 128), idesc_o,
+                           (i > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (!warp_wait(&pready[2 + t], par, p.status)) return false;
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int kk = kFPart1 / 16; kk < kFK / 16; ++kk)
+            pf_umma_tmem_a(pt + 128u, pt + static_cast<uint32_t>(kk * 8), vd + static_cast<uint32_t>(kk * 128), idesc_o,
+                           1u);
+          if (t == 1) umma_commit(&vempty[s]);
+        }
+        return true;
+      };
+      bool committed0 = false, committed1 = false;
+      if (ok && nk1 > 0) {
+        ok = warp_wait(&kfull[0], 0u, p.status);
+        if (ok && nk0 > 0) issue_s(0, 0);
+        if (ok) issue_s(1, 0);
+      }
+      int sv = 0, sk = 1;  // V stage of i, K stage of i + 1
+      uint32_t phv = 0u, phk = 0u;
+      for (int i = 0; ok && i < nk1; ++i) {
+        const bool more = i + 1 < nk1;
+        ok = warp_wait(&vfull[sv], phv, p.status) && (!more || warp_wait(&kfull[sk], phk, p.status));
+        if (!ok) break;
+        if (i < nk0) {
+          if (!(ok = issue_pv(0, i, sv))) break;
+          if (i == nk0 - 1) {
+            if (lead) umma_commit(&ofull[0]);
+            committed0 = true;
+          } else {
+            issue_s(0, sk);  // overwrites the P that the P·V above reads: issued after it
+          }
+        }
+        if (!(ok = issue_pv(1, i, sv))) break;
+        if (!more) {
+          if (lead) umma_commit(&ofull[1]);
+          committed1 = true;
+        } else {
+          issue_s(1, sk);
+        }
+        if (++sv == NV) {
+          sv = 0;
+          phv ^= 1u;
+        }
+        if (++sk == NK) {
+          sk = 0;
+          phk ^= 1u;
         }
       }
       // also after a failure: each output barrier covers every MMA issued
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (!committed[t]) umma_commit(&ofull[t]);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) mbar_wait(&ofull[t], 0u, p.status);
+      if (lead && !committed0) umma_commit(&ofull[0]);
+      if (lead && !committed1) umma_commit(&ofull[1]);
+      warp_wait(&ofull[0], 0u, p.status);
+      warp_wait(&ofull[1], 0u, p.status);
     }
   } else if (E && warp >= 12) {
     // ------------------------------------------------------------ codes to f16
-    reg_dec<80>();
+    reg_dec<64>();
     const int tid = threadIdx.x - 384;
     constexpr int CPR = DH / 16;  // 16-code chunks of a row
+    // A warp takes 32 / CPR rows at a time. At dh = 128 eight lanes read four chunks of one row and the
+    // other four of the next, and write two rows of different swizzle parity: every phase of the read
+    // and of both writes meets eight different 16-byte banks.
     auto convert = [&](const uint8_t* raw, uint8_t* dst, int valid) {
 #pragma unroll 4
       for (int u = tid; u < kFK * CPR; u += 128) {
-        const int row = u / CPR, cc = u - row * CPR;
-        uint4 w = *reinterpret_cast<const uint4*>(raw + u * 16);
-        if (row >= valid) w = make_uint4(0u, 0u, 0u, 0u);
-        const uint4 a = make_uint4(e4m3x2_to_f16x2(w.x & 0xffffu), e4m3x2_to_f16x2(w.x >> 16),
-                                   e4m3x2_to_f16x2(w.y & 0xffffu), e4m3x2_to_f16x2(w.y >> 16));
-        const uint4 d = make_uint4(e4m3x2_to_f16x2(w.z & 0xffffu), e4m3x2_to_f16x2(w.z >> 16),
-                                   e4m3x2_to_f16x2(w.w & 0xffffu), e4m3x2_to_f16x2(w.w >> 16));
+        int row = u / CPR, cc = u - row * CPR;
+        if (CPR == 8) {
+          row = (u >> 4) * 2 + ((u >> 2) & 1);
+          cc = (u & 3) + 4 * (((u >> 2) ^ (u >> 3)) & 1);
+        }
+        uint4 w = *reinterpret_cast<const uint4*>(raw + row * DH + cc * 16);
+        if (valid < kFK && row >= valid) w = make_uint4(0u, 0u, 0u, 0u);
         uint8_t* box = dst + (cc >> 2) * 16384 + row * 128;
         const int c0 = (2 * cc) & 7, sw = row & 7;
-        // lanes of the second box write their odd chunk first: eight lanes, eight banks
-        const bool odd = (cc >> 2) != 0;
-        *reinterpret_cast<uint4*>(box + (((c0 + (odd ? 1 : 0)) ^ sw) << 4)) = odd ? d : a;
-        *reinterpret_cast<uint4*>(box + (((c0 + (odd ? 0 : 1)) ^ sw) << 4)) = odd ? a : d;
+        *reinterpret_cast<uint4*>(box + ((c0 ^ sw) << 4)) =
+            make_uint4(e4m3x2_to_f16x2(w.x & 0xffffu), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y & 0xffffu),
+                       e4m3x2_to_f16x2(w.y >> 16));
+        *reinterpret_cast<uint4*>(box + (((c0 + 1) ^ sw) << 4)) =
+            make_uint4(e4m3x2_to_f16x2(w.z & 0xffffu), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w & 0xffffu),
+                       e4m3x2_to_f16x2(w.w >> 16));
       }
     };
     for (int i = 0; i < nkt; ++i) {
-      const int s = i % NS, valid = Lz - (kt0 + i) * kFK;
-      const uint32_t ph = static_cast<uint32_t>((i / NS) & 1), rph = static_cast<uint32_t>(i & 1);
-      bool got = mbar_wait(&rfull[0], rph, p.status) && (i < NS || mbar_wait(&kempty[s], ph ^ 1u, p.status));
-      if (!__all_sync(0xffffffffu, got)) break;
-      convert(rk, ks + s * T, valid);
+      const int s = i % NV, sr = i % NR;
+      if (!warp_wait(&rfull[sr], static_cast<uint32_t>(i / NR) & 1u, p.status) ||
+          (i >= NV && !warp_wait(&vempty[s], static_cast<uint32_t>(i / NV - 1) & 1u, p.status)))
+        break;
+      convert(rv + sr * C::kRaw, vs + s * T, Lz - (kt0 + i) * kFK);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&rempty[0]);
-        mbar_arrive(&kfull[s]);
-      }
-      got = mbar_wait(&rfull[1], rph, p.status) && (i < NS || mbar_wait(&vempty[s], ph ^ 1u, p.status));
-      if (!__all_sync(0xffffffffu, got)) break;
-      convert(rv, vs + s * T, valid);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&rempty[1]);
+        mbar_arrive(&rempty[sr]);
         mbar_arrive(&vfull[s]);
       }
     }
   } else {
     // ------------------------------------------------------------ softmax of row tile t
-    reg_inc<E ? 192 : 224>();
+    reg_inc<E ? 192 : 216>();
     const int t = (warp - 4) >> 2;
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;  // row of the tile = TMEM lane
@@ -395,42 +460,59 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     const uint32_t ts = tmem + t * kFTmemPerTile, tmem_o = ts + 128u;
     const int q0 = tile_q0(t), nkt_t = tile_end(t) - kt0;
     const int nkt_below = t > 0 ? tile_end(0) - kt0 : 0;  // key tiles that the lower tile attends too
-    const int qi = q0 + row / p.G, head = h * p.G + row % p.G;
+    auto div_g = [&](int x) { return static_cast<int>((static_cast<uint32_t>(x) * p.g_inv) >> 16); };
+    const int qi = q0 + div_g(row), head = h * p.G + row - div_g(row) * p.G;
     const bool live = q0 >= 0 && row < p.QPT * p.G && qi < n;
     const int pos = live ? len + qi : -1;  // a row without a query attends nothing
     float fq = p.scale_log2;
-    // this thread's query row into the Q tile (zeros where there is none)
+    // The warp's 32 query rows into the Q tile, zeros where there is none: LR lanes read one row, so that
+    // a load takes whole lines (a row per thread took 7,000 cycles at dh = 128, this 1,500).
     {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(r.row0) + (live ? qi : 0)) * p.q_stride +
-                                                        static_cast<int64_t>(head) * DH);
-      uint4 w[DH / 8];
+      constexpr int LR = DH / 8, RI = 32 / LR;  // lanes of a row, rows of a load
+      const int c = lane % LR;
+      uint4 wv[32 / RI];
 #pragma unroll
-      for (int c = 0; c < DH / 8; ++c) w[c] = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      if (E) {
-        uint32_t amax = 0u;
-#pragma unroll
-        for (int c = 0; c < DH / 8; ++c) {
-          const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) amax = max(amax, max(x[k] & 0x7fffu, (x[k] >> 16) & 0x7fffu));
-        }
-        const int e = max(-126, min(126, static_cast<int>(amax >> 7) - 127));
-        const float inv = exp2_int(-e);
-        fq *= exp2_int(e);
-#pragma unroll
-        for (int c = 0; c < DH / 8; ++c) {
-          uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __half2 hv = __floats2half2_rn(bf16lo(x[k]) * inv, bf16hi(x[k]) * inv);
-            x[k] = *reinterpret_cast<const uint32_t*>(&hv);
-          }
-          w[c] = make_uint4(x[0], x[1], x[2], x[3]);
-        }
+      for (int k = 0; k < 32; k += RI) {
+        const int rr = quarter * 32 + k + lane / LR, qd = div_g(rr), rq = q0 + qd;
+        wv[k / RI] = make_uint4(0u, 0u, 0u, 0u);
+        if (q0 >= 0 && rr < p.QPT * p.G && rq < n)
+          wv[k / RI] = __ldg(reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(r.row0) + rq) * p.q_stride +
+                                                            (static_cast<int64_t>(h) * p.G + rr - qd * p.G) * DH) + c);
       }
 #pragma unroll
-      for (int c = 0; c < DH / 8; ++c)
-        *reinterpret_cast<uint4*>(qs + t * T + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = w[c];
+      for (int k = 0; k < 32; k += RI) {
+        const int rr = quarter * 32 + k + lane / LR;
+        const uint4 w = wv[k / RI];
+        if (!E) {
+          *reinterpret_cast<uint4*>(qs + t * T + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = w;
+          continue;
+        }
+        // in units that bring the row's largest magnitude to [128, 256): a high and a low e4m3 part hold
+        // the 8 bits of a bf16 exactly down to 2^-10 of it, and 2^-17 of it is the error below
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        uint32_t amax = 0u;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) amax = max(amax, max(x[u] & 0x7fffu, (x[u] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int o = 1; o < LR; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e = max(-118, min(126, static_cast<int>(amax >> 7) - 127));
+        const float inv = exp2_int(7 - e);
+        float f = exp2_int(e) * 0.0078125f * p.scale_log2;
+        if (amax >= 0x7f80u) f = __uint_as_float(0x7fc00000u);  // e4m3 has no infinity
+        f = __shfl_sync(0xffffffffu, f, (lane % RI) * LR);
+        if (lane / RI == k / RI) fq = f;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float y0 = bf16lo(x[u]) * inv, y1 = bf16hi(x[u]) * inv;
+          hi[u] = to_e4m3x2(y0, y1);
+          const float2 g = e4m3x2_to_float2(hi[u]);
+          lo[u] = to_e4m3x2(y0 - g.x, y1 - g.y);
+        }
+        uint8_t* at = qs + t * T + rr * DH + (((c >> 1) ^ (DH == 128 ? rr & 7 : (rr >> 1) & 3)) << 4) + (c & 1) * 8;
+        *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+        *reinterpret_cast<uint2*>(at + T / 2) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qbar);
@@ -451,7 +533,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int i = 0; i < nkt_t; ++i) {
-      const int s = i % NS;
+      const int s = i % NV;
       const float ks_lane = ks_next, lv_lane = lv_next;
       if (E) fetch(i + 1, ks_next, lv_next);
       if (!__all_sync(0xffffffffu, mbar_wait(&sfull[t], static_cast<uint32_t>(i) & 1u, p.status))) {
@@ -469,8 +551,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       // scale's exponent lv, so that P stays in f16's range whatever the pages' scales are. P of key t
       // is 2^(s_t + e), e = lv - m, and l adds P·2^-lv. Where a group's largest P is below 2^-60 (its
       // f16 is zero) e is raised to keep the fp32 sum from underflowing.
-      float alpha = 1.f;
       auto advance = [&](float mt) {
+        float alpha = 1.f;
         if (m == -INFINITY) {
           m = mt;
         } else if (mt > m + kFLazyLog2) {
@@ -478,17 +560,31 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           m = mt;
           l *= alpha;
         }
+        // O is rescaled before P is handed over. The tensor cores are done with it: S of this key tile
+        // was issued after the last P·V, and its barrier covers that too.
+        if (i >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          for (int c = 0; c < DH; c += 16) {
+            float v[16];
+            tmem_ld16(tmem_o + lrow + static_cast<uint32_t>(c), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] *= alpha;
+            tmem_st16(tmem_o + lrow + static_cast<uint32_t>(c), v);
+          }
+        }
       };
-      // P of keys 32 q .. 32 q + 31 to tensor memory; returns their sum
+      // P of keys 32 q .. 32 q + 31 to tensor memory; the sums of either half
       auto weights = [&](int q, float f, float e0, float e1, float& sum0, float& sum1) {
         uint32_t pk[16];
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t s2[2] = {0ull, 0ull};
+        const uint64_t ff = pack2(f, f);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           const float e = c < 8 ? e0 : e1;
-          const float a = pf_ex2(fmaf(sc[32 * q + 2 * c], f, e));
-          const float bb = pf_ex2(fmaf(sc[32 * q + 2 * c + 1], f, e));
-          s4[(c & 1) + (c < 8 ? 0 : 2)] += a + bb;
+          float x0, x1;
+          unpack2(ffma2(pack2(sc[32 * q + 2 * c], sc[32 * q + 2 * c + 1]), ff, pack2(e, e)), x0, x1);
+          const float a = pf_ex2(x0), bb = pf_ex2(x1);
+          s2[c >> 3] = fadd2(s2[c >> 3], pack2(a, bb));
           if (E) {
             const __half2 hv = __floats2half2_rn(a, bb);
             pk[c] = *reinterpret_cast<const uint32_t*>(&hv);
@@ -498,9 +594,28 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           }
         }
         pf_tmem_st16(ts + lrow + static_cast<uint32_t>(16 * q), pk);
-        sum0 = s4[0] + s4[1];
-        sum1 = s4[2] + s4[3];
+        sum0 = unpack_sum(s2[0]);
+        sum1 = unpack_sum(s2[1]);
       };
+      // hands a part of P (and, before the first, the zeroed V rows and O) to the MMA warp
+      auto hand_over = [&](int part) {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pready[2 * part + t]);
+      };
+      // bf16: key rows from Lz on are zeroed in V (thread r takes key row r, once the tile's V has
+      // landed) by the lowest tile that attends this key tile
+      if (!E && k0 + kFK > Lz && i >= nkt_below) {
+        if (k0 + row >= Lz && mbar_wait(&vfull[s], static_cast<uint32_t>(i / NV) & 1u, p.status)) {
+          uint8_t* vrow = vs + s * T + row * 128;
+#pragma unroll
+          for (int k = 0; k < DHB; ++k)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + k * 16384 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
       float ksu = 1.f, lvu = 0.f;
       bool uniform = true;  // one scale pair for all pages of the tile
       if (E) {
@@ -514,10 +629,15 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kFK; ++c) sc[c] = (k0 + c <= pos) ? sc[c] : -INFINITY;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[4] = {sc[0], sc[1], sc[2], sc[3]};
 #pragma unroll
-        for (int c = 0; c < kFK; ++c) mx[c & 3] = fmaxf(mx[c & 3], sc[c]);
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+        for (int c = 4; c + 8 <= kFK; c += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], sc[c + k], sc[c + 4 + k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], sc[kFK - 4 + k]);
+        const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
         advance(mt + lvu);
         const float mm = m == -INFINITY ? 0.f : m;
         float e = lvu - mm;
@@ -528,7 +648,9 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           float s0, s1;
           weights(q, f, e, e, s0, s1);
           total += s0 + s1;
+          if (32 * (q + 1) == kFPart1) hand_over(0);
         }
+        hand_over(1);
         l += E ? total * pf_ex2(-mm - e) : total;
       } else {
         float lv[kFK / 16], mg[kFK / 16], top = -INFINITY;
@@ -557,82 +679,78 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           }
           weights(q, 1.f, e[0], e[1], s2[0], s2[1]);
           l += s2[0] * pf_ex2(-mm - e[0]) + s2[1] * pf_ex2(-mm - e[1]);
+          if (32 * (q + 1) == kFPart1) hand_over(0);
         }
+        hand_over(1);
       }
-      if (i >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // O is rescaled once the previous key tile's P·V has completed
-        if (!__all_sync(0xffffffffu, mbar_wait(&pfree[t], static_cast<uint32_t>(i - 1) & 1u, p.status))) {
-          tmem_wait_st();
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        for (int c = 0; c < DH; c += 16) {
-          float v[16];
-          tmem_ld16(tmem_o + lrow + static_cast<uint32_t>(c), v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] *= alpha;
-          tmem_st16(tmem_o + lrow + static_cast<uint32_t>(c), v);
-        }
-      }
-      tmem_wait_st();
-      // bf16: key rows from Lz on are zeroed in V (thread r takes key row r, once
-      // the tile's V has landed) by the lowest tile that attends this key tile
-      if (!E && k0 + kFK > Lz && i >= nkt_below && k0 + row >= Lz) {
-        if (mbar_wait(&vfull[s], static_cast<uint32_t>(i / NS) & 1u, p.status)) {
-          uint8_t* vrow = vs + s * T + row * 128;
-#pragma unroll
-          for (int k = 0; k < DHB; ++k)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + k * 16384 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-      if (!E) fence_proxy_async_smem();  // zeroed V rows are read by the tensor cores
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pready[t]);
     }
     // ------------------------------------------------------------ o = O / l, or the split's partial
     bool got = ok;
     if (nkt_t > 0) got = ok && __all_sync(0xffffffffu, mbar_wait(&ofull[t], 0u, p.status));
     tc_fence_after();
     const bool broken = pos >= *s_bad;
-    const int64_t orow = (static_cast<int64_t>(r.row0) + (live ? qi : 0)) * p.Hq + head;
+    // 128 bytes of every row at a time go through the warp's part of the Q tile (no MMA reads it any
+    // more), so that eight lanes store one whole line
+    uint8_t* stage = qs + t * T + quarter * 4096;
+    auto put_lines = [&](const uint4 (&w)[8], uint8_t* base, int64_t row_bytes) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = w[c];
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 32; k += 4) {
+        const int rl = k + (lane >> 3), rr = quarter * 32 + rl, qd = div_g(rr), rq = q0 + qd;
+        const uint4 y = *reinterpret_cast<const uint4*>(stage + rl * 128 + (((lane & 7) ^ (rl & 7)) << 4));
+        if (rr < p.QPT * p.G && rq < n)
+          *reinterpret_cast<uint4*>(base + ((static_cast<int64_t>(r.row0) + rq) * p.Hq + h * p.G + rr - qd * p.G) * row_bytes +
+                                    (lane & 7) * 16) = y;
+      }
+      __syncwarp();
+    };
     if (p.splits == 1) {
       if (q0 >= 0) {
         const float inv = !got || broken || l == 0.f ? 0.f : 1.f / l;
-        for (int c = 0; c < DH; c += 16) {
-          float v[16];
-          tmem_ld16(tmem_o + lrow + static_cast<uint32_t>(c), v);
+#pragma unroll 1
+        for (int c = 0; c < DH; c += 64) {
+          uint4 w[8];
+          float v[64];
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            tmem_ld16(tmem_o + lrow + static_cast<uint32_t>(c + 16 * g), *reinterpret_cast<float(*)[16]>(v + 16 * g));
           tmem_wait_ld();
-          if (live) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
             uint32_t y[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = broken ? 0u : pack_bf16x2(v[2 * k] * inv, v[2 * k + 1] * inv);
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * DH + c);
-            dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-            dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            for (int k = 0; k < 8; ++k)
+              y[k] = broken ? 0u : pack_bf16x2(v[16 * g + 2 * k] * inv, v[16 * g + 2 * k + 1] * inv);
+            w[2 * g] = make_uint4(y[0], y[1], y[2], y[3]);
+            w[2 * g + 1] = make_uint4(y[4], y[5], y[6], y[7]);
           }
+          put_lines(w, reinterpret_cast<uint8_t*>(p.out + c), DH * 2);
         }
       }
     } else if (q0 >= 0) {
-      const int64_t prow = static_cast<int64_t>(split) * p.rows * p.Hq + orow;
+      const int64_t first = static_cast<int64_t>(split) * p.rows * p.Hq;
       if (live) {
+        const int64_t prow = first + (static_cast<int64_t>(r.row0) + qi) * p.Hq + head;
         p.ws_ml[prow * 2] = nkt_t > 0 && got ? m : -INFINITY;
         p.ws_ml[prow * 2 + 1] = broken ? -1.f : nkt_t > 0 && got ? l : 0.f;
       }
       if (nkt_t > 0) {
-        for (int c = 0; c < DH; c += 16) {
-          float v[16];
-          tmem_ld16(tmem_o + lrow + static_cast<uint32_t>(c), v);
-          tmem_wait_ld();
-          if (live) {
+#pragma unroll 1
+        for (int c = 0; c < DH; c += 32) {
+          uint4 w[8];
 #pragma unroll
-            for (int k = 0; k < 16; k += 4)
-              *reinterpret_cast<float4*>(p.ws_o + prow * DH + c + k) =
-                  make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          for (int g = 0; g < 2; ++g) {
+            float v[16];
+            tmem_ld16(tmem_o + lrow + static_cast<uint32_t>(c + 16 * g), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[4 * g + k] = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
+                                        __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
           }
+          put_lines(w, reinterpret_cast<uint8_t*>(p.ws_o + first * DH + c), DH * 4);
         }
       }
     }
@@ -765,6 +883,7 @@ cudaError_t launch_paged_prefill(const slim_paged_cache& c, const void* q, int64
   p.Hq = Hq;
   p.G = f.G;
   p.QPT = f.QPT;
+  p.g_inv = (65536u + static_cast<uint32_t>(f.G) - 1u) / static_cast<uint32_t>(f.G);
   p.pairs = f.pairs;
   p.splits = f.splits;
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -781,6 +900,9 @@ cudaError_t launch_paged_prefill(const slim_paged_cache& c, const void* q, int64
     return c.dh == 64 ? launch_pf<false, 1>(kmap, vmap, p, st, launches)
                       : launch_pf<false, 2>(kmap, vmap, p, st, launches);
   }
+  // e4m3 keys go to the MMA as they are: whole rows, in the swizzle of their length
+  if (!encode_tmap_2d_u8(&kmap, c.kpages, c.dh, static_cast<uint64_t>(c.num_pages) * c.Hkv * c.page, c.dh, c.page))
+    return cudaErrorInvalidValue;
   return c.dh == 64 ? launch_pf<true, 1>(kmap, vmap, p, st, launches)
                     : launch_pf<true, 2>(kmap, vmap, p, st, launches);
 }

@@ -138,6 +138,10 @@ cudaError_t launch_front(const void* x, const void* W_Q, const void* W_K, float*
 bool encode_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                          uint32_t box_inner, uint32_t box_outer, bool swizzle128);
 
+// Rows of `inner` bytes (64 or 128) as a 2-D byte map with the swizzle of that length.
+bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                       uint32_t box_outer);
+
 // General 3-D bf16 tiled map: dims {d0, d1, d2} (d0 innermost, contiguous), byte strides s1, s2 of
 // dims 1 and 2, box {b0, b1, b2}, 128-byte swizzle (b0 * 2 must be <= 128).
 bool encode_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
