@@ -101,7 +101,7 @@ int slim_mha_paged_gather(const slim_paged_cache* cache, const int32_t* starts, 
 
 size_t slim_mha_paged_decode_workspace_bytes(const slim_paged_cache* cache, int Hq) {
   if (check_cache(cache) != SLIM_OK || Hq < 1 || Hq > 8192 || Hq % cache->Hkv) return 0;
-  return paged_decode_ws_bytes(*cache, Hq);
+  return paged_rows_ws_bytes(*cache, Hq / cache->Hkv);
 }
 
 int slim_mha_paged_decode(const slim_paged_cache* cache, const void* q, int64_t q_stride, const int32_t* lens,
@@ -112,10 +112,10 @@ int slim_mha_paged_decode(const slim_paged_cache* cache, const void* q, int64_t 
   if (!lens || !aligned(lens, 4) || !out || !aligned(out, 16) || !dev_status) return SLIM_EINVAL;
   if (rows_extra != 0 && rows_extra != 1) return SLIM_EINVAL;
   if (Hq < 1 || Hq > 8192 || Hq % cache->Hkv || !check_rows(q, q_stride, Hq, cache->dh)) return SLIM_EINVAL;
-  if (!workspace || !aligned(workspace, 256) || ws_bytes < paged_decode_ws_bytes(*cache, Hq)) return SLIM_EWORKSPACE;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < paged_rows_ws_bytes(*cache, Hq / cache->Hkv)) return SLIM_EWORKSPACE;
   int launches = 0;
-  const cudaError_t e = launch_paged_decode(*cache, q, q_stride, lens, rows_extra, Hq, t_hint, out, workspace,
-                                            dev_status, static_cast<cudaStream_t>(stream), &launches);
+  const cudaError_t e = launch_paged_rows(*cache, q, q_stride, nullptr, lens, cache->B, 1, rows_extra, Hq, t_hint, out,
+                                          workspace, dev_status, static_cast<cudaStream_t>(stream), &launches);
   return finish(e, launches);
 }
 

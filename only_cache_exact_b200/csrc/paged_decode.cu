@@ -1,5 +1,6 @@
-// slim_mha_paged_decode: attention of one query row per sequence over a paged
-// K+V cache in bf16 or e4m3.
+// Attention of a few query rows per sequence over a paged K+V cache in bf16 or
+// e4m3: slim_mha_paged_decode (one row), and slim_mha_paged_prefill where the
+// rows that share a key head are at most 32 (a few proposed tokens).
 //
 // Mathematics, per sequence and key/value head, for the G query heads that
 // share it: s_t = q·K_t·log2(e)/sqrt(dh), m = max s, p_t = 2^(s_t - m),
@@ -9,11 +10,11 @@
 // P_t = 2^(s_t + lv - m) with m the running maximum of s + lv, which keeps them
 // in f16's range whatever the pages' scales are; l adds P_t·2^-lv.
 //
-// Bound: memory. Each cached element is read once and meets 4·G flops per 2 or
-// 1 bytes; the row count of every matrix product is 8 or 16 (padded heads), so
-// the warp-level MMA is ample and needs no tile to be filled. Heads are its N
-// and tokens its M (S^T = K·q^T) and then columns its M (O^T = V^T·p^T), so
-// that up to 8 heads cost half of what 16-row tiles of heads would: K and V
+// Bound: memory. Each cached element is read once and meets 4 flops per row (a
+// query and head) for its 2 or 1 bytes; the row count of every matrix product
+// is 8 to 32, so the warp-level MMA is ample and needs no tile to be filled. Rows
+// are its N and keys its M (S^T = K·q^T) and then columns its M (O^T = V^T·p^T),
+// so that up to 8 rows cost half of what 16-row tiles of them would: K and V
 // are the A operands straight from shared memory by ldmatrix, and the
 // probabilities go from the result's layout to the operand's by movmatrix,
 // without shared memory. e4m3 codes become f16 pairs exactly (one cvt per
@@ -47,8 +48,10 @@ struct PagedDecodeParams {
   const __nv_bfloat16* q;
   int64_t q_stride;
   const int32_t* lens;
-  int extra;
-  int Hq, G, NG;  // G query heads per key head, in NG groups
+  const int32_t* starts;  // packed query rows of each sequence; nullptr: row b of sequence b
+  int64_t rows, max_new;
+  int extra;      // rows that lens does not count (starts == nullptr)
+  int Hq, G, NG;  // G query heads per key head; rows of a (sequence, key head) in NG groups
   int HG;         // Hkv * NG work sequences per cache sequence
   __nv_bfloat16* out;
   float* ws_o;     // [ctas][kDSlots][heads][dh]
@@ -104,18 +107,32 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Attended rows of sequence b, 0 where it is skipped (bits says why).
-__device__ __forceinline__ int attended(const PagedDecodeParams& p, int b, int& bits) {
+// A sequence's query rows and keys. Row j (of n) sits at position len + j - n and attends the keys
+// up to its own; keys is 0 where there is nothing to do or the sequence is skipped (bits says why).
+struct DecSeq {
+  int row0, n, keys, bits;
+  bool span;  // rows row0 .. row0+n-1 may be written
+};
+__device__ __forceinline__ DecSeq dec_seq(const PagedDecodeParams& p, int b) {
+  DecSeq s;
+  if (p.starts) {
+    const PagedRows r = paged_rows(p.starts, p.lens, b, p.rows, p.max_new, p.c.cap, p.c.cap);
+    s.row0 = r.row0;
+    s.n = r.n;
+    s.bits = r.bits;
+    s.span = r.span;
+    s.keys = r.bits || r.n == 0 ? 0 : r.len + r.n;
+    return s;
+  }
   const int L = __ldg(p.lens + b);
-  if (L < 0 || static_cast<int64_t>(L) > p.c.cap) {
-    bits |= SLIM_DEV_BADLEN;
-    return 0;
-  }
-  if (static_cast<int64_t>(L) + p.extra > p.c.cap) {
-    bits |= SLIM_DEV_OVERFLOW;
-    return 0;
-  }
-  return L + p.extra;
+  s.row0 = b;
+  s.n = 1;
+  s.span = true;
+  s.bits = L < 0 || static_cast<int64_t>(L) > p.c.cap                ? SLIM_DEV_BADLEN
+           : static_cast<int64_t>(L) + p.extra > p.c.cap ? SLIM_DEV_OVERFLOW
+                                                                     : 0;
+  s.keys = s.bits ? 0 : L + p.extra;
+  return s;
 }
 
 // CTA c of A owns line tiles [c·X/A, (c+1)·X/A); inside it warp w owns `chunk` tiles from w·chunk.
@@ -159,7 +176,7 @@ template <bool E, int DH, int NT>
 struct DecCfg {
   static constexpr int kRowB = DH * (E ? 1 : 2);           // bytes of a row
   static constexpr int kTileB = 16 * kRowB;                // K (or V) of a tile
-  static constexpr int kTT = kTileB >= 4096 ? 1 : 2;       // tiles of a stage
+  static constexpr int kTT = kTileB >= 4096 || NT == 4 ? 1 : 2;  // tiles of a stage (32 rows: registers)
   static constexpr int kStageB = 2 * kTT * kTileB;
   static constexpr int kStages = kDRing / kStageB;
   static constexpr int kHeads = 8 * NT;
@@ -187,6 +204,12 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
   pdl_wait_primary();
 
   // ---------------------------------------------------------------- this warp's share
+  auto zero_rows = [&](const DecSeq& q) {
+    if (!q.span) return;
+    const int64_t n = static_cast<int64_t>(q.n) * p.Hq * DH / 8;
+    for (int64_t i = threadIdx.x; i < n; i += kDThreads)
+      reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(q.row0) * p.Hq * DH)[i] = make_uint4(0u, 0u, 0u, 0u);
+  };
   DecCursor cur;
   if (p.split) {
     if (warp == 0) {
@@ -194,7 +217,12 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
       int bits = 0;
       for (int base = 0; base < p.c.B; base += 32) {
         const int b = base + lane;
-        const uint32_t t = b < p.c.B ? static_cast<uint32_t>((attended(p, b, bits) + 15) >> 4) : 0u;
+        uint32_t t = 0u;
+        if (b < p.c.B) {
+          const DecSeq q = dec_seq(p, b);
+          bits |= q.bits;
+          t = static_cast<uint32_t>((q.keys + 15) >> 4);
+        }
         uint32_t x = t;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -234,27 +262,22 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
     }
     // nothing to attend to: zero rows, dealt to the CTAs
     for (int b = blockIdx.x; b < p.c.B; b += gridDim.x)
-      if (s_pre[b + 1] == s_pre[b])
-        for (int i = threadIdx.x; i < p.Hq * DH / 8; i += kDThreads)
-          reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(b) * p.Hq * DH)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (s_pre[b + 1] == s_pre[b]) zero_rows(dec_seq(p, b));
   } else {
     cur.b = blockIdx.x / p.HG;
     cur.hg = blockIdx.x - cur.b * p.HG;
-    int bits = 0;
-    cur.T = (attended(p, cur.b, bits) + 15) >> 4;
-    if (bits && cur.hg == 0 && threadIdx.x == 0) atomicOr(p.status, bits);
+    const DecSeq q = dec_seq(p, cur.b);
+    cur.T = (q.keys + 15) >> 4;
+    if (q.bits && cur.hg == 0 && threadIdx.x == 0) atomicOr(p.status, q.bits);
     const int chunk = (cur.T + kDW - 1) / kDW;
     cur.tile = warp * chunk;
     cur.left = min(chunk, cur.T - cur.tile);
-    if (cur.T == 0 && cur.hg == 0)
-      for (int i = threadIdx.x; i < p.Hq * DH / 8; i += kDThreads)
-        reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(cur.b) * p.Hq * DH)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (cur.T == 0 && cur.hg == 0) zero_rows(q);
   }
 
   uint8_t* ring = dec_smem + warp * kDRing;
   const uint32_t ring_u = smem_u32(ring);
   float* my_scale = s_scale + warp * C::kStages * C::kTT * 2;
-  bool bad = false;  // a page number of the segment being loaded is outside the pool
 
   // ---------------------------------------------------------------- loads
   // The load side runs kStages - 1 stages ahead, across segments. Page numbers of 32 tiles at a time
@@ -274,30 +297,30 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
   };
   auto seg_start = [&]() {
     l_tile = ls.tile;
-    l_nb = __ldg(p.lens + ls.b) + p.extra;
+    l_nb = dec_seq(p, ls.b).keys;
     l_h = ls.hg / p.NG;
     l_head = l_h * p.c.head_bytes;
     window();
   };
   if (l_more) seg_start();
-  uint32_t bad_mask = 0u;  // bit s: stage s holds a tile of a page outside the pool
+  uint32_t bad_mask = 0u;  // bit stage * kTT + k: that tile's page is outside the pool; it is all zeros
   auto issue = [&](int stage) {
     if (l_more) {
       if (l_tile - l_win > 32 - C::kTT) window();
-      bool stage_bad = false;
 #pragma unroll
       for (int k = 0; k < C::kTT; ++k) {
         const int t = l_tile + k;
         if (t >= ls.end) break;
         int id = __shfl_sync(0xffffffffu, l_id, t - l_win);
-        if (id < 0 || id >= p.c.num_pages) {
-          stage_bad = true;
-          id = 0;
-        }
+        const bool page_bad = id < 0 || id >= p.c.num_pages;
+        if (page_bad) id = 0;
+        const uint32_t bit = 1u << (stage * C::kTT + k);
+        bad_mask = page_bad ? bad_mask | bit : bad_mask & ~bit;
         const int64_t row = (static_cast<int64_t>(t) * 16) & ((1 << p.c.page_shift) - 1);
         const int64_t off = id * p.c.page_bytes + l_head + row * C::kRowB;
         const uint32_t dst = ring_u + stage * C::kStageB + k * 2 * C::kTileB;
-        const int valid = l_nb - t * 16;  // rows of the tile that exist; the others are filled with zeros
+        // rows of the tile that exist; the others are filled with zeros
+        const int valid = page_bad ? 0 : l_nb - t * 16;
 #pragma unroll
         for (int i = 0; i < C::kTileB / 512; ++i) {
           const int ch = i * 32 + lane, r = ch / (C::kRowB / 16), c = ch % (C::kRowB / 16);
@@ -310,7 +333,6 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
           cp_async4(smem_u32(my_scale + (stage * C::kTT + k) * 2 + lane), sc);
         }
       }
-      bad_mask = stage_bad ? bad_mask | (1u << stage) : bad_mask & ~(1u << stage);
       l_tile += C::kTT;
       if (l_tile >= ls.end) {
         l_more = ldc.next(ls, s_pre, p.HG);
@@ -327,16 +349,23 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
   DecSeg sg;
   int stage = 0;
   while (cur.next(sg, s_pre, p.HG)) {
-    const int kvh = sg.hg / p.NG, head0 = kvh * p.G + (sg.hg - kvh * p.NG) * C::kHeads;
-    const int nh = min(C::kHeads, (kvh + 1) * p.G - head0);
-    const int nb = __ldg(p.lens + sg.b) + p.extra;
+    const int kvh = sg.hg / p.NG, r0g = (sg.hg - kvh * p.NG) * C::kHeads;  // first row of the group
+    const DecSeq sq = dec_seq(p, sg.b);
+    const int nh = min(C::kHeads, sq.n * p.G - r0g);
+    // row rr of the (sequence, key head) is query rr / G of the sequence and head rr % G of the key head
+    auto row_of = [&](int rr, int& j) {
+      j = rr / p.G;
+      return (static_cast<int64_t>(sq.row0) + j) * p.Hq + static_cast<int64_t>(kvh) * p.G + (rr - j * p.G);
+    };
     // the query as the B operand: head lg of each group of 8, zero past the group's heads
     uint32_t qf[NT][DH / 16][2];
     float hs[NT][2];  // score factor of heads 2 lq and 2 lq + 1
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int hd = n * 8 + lg;
-      const __nv_bfloat16* src = p.q + sg.b * p.q_stride + static_cast<int64_t>(head0 + (hd < nh ? hd : 0)) * DH;
+      const int rr = r0g + (hd < nh ? hd : 0), j = rr / p.G;
+      const __nv_bfloat16* src = p.q + (static_cast<int64_t>(sq.row0) + j) * p.q_stride +
+                                 (static_cast<int64_t>(kvh) * p.G + (rr - j * p.G)) * DH;
       if (E) {
         uint2 w[DH / 16];
         uint32_t amax = 0u;
@@ -370,12 +399,19 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
-    bad = false;
+    int bad_pos = 0x7fffffff;  // first key of the segment whose page is outside the pool
+    int lim[NT][2];            // keys that rows 2 lq and 2 lq + 1 attend
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lim[n][i] = sq.keys - sq.n + 1 + min(r0g + n * 8 + 2 * lq + i, sq.n * p.G - 1) / p.G;
 
     for (int t = sg.tile; t < sg.end; t += C::kTT) {
       cp_async_wait<C::kStages - 2>();
       __syncwarp();  // also: every lane is done with the stage before this one, which is filled next
-      bad |= (bad_mask >> stage) & 1u;
+#pragma unroll
+      for (int k = 0; k < C::kTT; ++k)
+        if (t + k < sg.end && ((bad_mask >> (stage * C::kTT + k)) & 1u)) bad_pos = min(bad_pos, (t + k) * 16);
       issue(stage == 0 ? C::kStages - 1 : stage - 1);
       const uint32_t kb = ring_u + stage * C::kStageB;
       const int tiles = min(C::kTT, sg.end - t);
@@ -425,7 +461,7 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float f = E ? hs[n][i & 1] * ks : hs[n][i & 1];
-            s[k][n][i] = k < tiles && r0 + (i >> 1) * 8 < nb ? s[k][n][i] * f : -INFINITY;
+            s[k][n][i] = k < tiles && r0 + (i >> 1) * 8 < lim[n][i & 1] ? s[k][n][i] * f : -INFINITY;
             mx[n][i & 1] = fmaxf(mx[n][i & 1], E ? s[k][n][i] + lv[k] : s[k][n][i]);
           }
         }
@@ -526,9 +562,9 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], sh);
-        if (bad) l[n][i] = -1.f;
+        if (bad_pos < lim[n][i]) l[n][i] = -1.f;
       }
-    if (bad && lane == 0) atomicOr(p.status, SLIM_DEV_BADPAGE);
+    if (bad_pos != 0x7fffffff && lane == 0) atomicOr(p.status, SLIM_DEV_BADPAGE);
     const bool whole = sg.tile == 0 && sg.end == sg.T;
     const bool last = cur.left <= 0;
     if (whole) {
@@ -539,11 +575,12 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
           const int hd = n * 8 + 2 * lq + (i & 1);
           if (hd >= nh) continue;
           const float f = l[n][i & 1] > 0.f || l[n][i & 1] != l[n][i & 1] ? 1.f / l[n][i & 1] : 0.f;
-          __nv_bfloat16* dst = p.out + (static_cast<int64_t>(sg.b) * p.Hq + head0 + hd) * DH;
+          int j;
+          __nv_bfloat16* dst = p.out + row_of(r0g + hd, j) * DH;
 #pragma unroll
           for (int c = 0; c < DH / 16; ++c) {
             const int col = 16 * c + (E ? 2 * lg + (i >> 1) : lg + (i >> 1) * 8);
-            dst[col] = __float2bfloat16_rn(bad ? 0.f : o[c][n][i] * f);
+            dst[col] = __float2bfloat16_rn(l[n][i & 1] < 0.f ? 0.f : o[c][n][i] * f);
           }
         }
     } else {
@@ -593,8 +630,9 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
     while (w1 < kDW && s_seq[w1] == seq) ++w1;
     const bool whole = s_seg[w0 * 4] == 0 && s_seg[(w1 - 1) * 4 + 1] == s_seg[w0 * 4 + 2];
     const int b = static_cast<int>(seq / p.HG), hg = static_cast<int>(seq - static_cast<int64_t>(b) * p.HG);
-    const int kvh = hg / p.NG, head0 = kvh * p.G + (hg - kvh * p.NG) * C::kHeads;
-    const int nh = min(C::kHeads, (kvh + 1) * p.G - head0);
+    const int kvh = hg / p.NG, r0g = (hg - kvh * p.NG) * C::kHeads;
+    const DecSeq sq = dec_seq(p, b);
+    const int nh = min(C::kHeads, sq.n * p.G - r0g);
     const int64_t slot = static_cast<int64_t>(blockIdx.x) * kDSlots + w0;
     for (int i = threadIdx.x; i < nh * DH; i += kDThreads) {
       const int hd = i / DH;
@@ -609,8 +647,9 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
         O = fmaf(f, reinterpret_cast<const float*>(dec_smem + w * kDRing)[i], O);
       }
       if (whole) {
-        p.out[(static_cast<int64_t>(b) * p.Hq + head0) * DH + i] =
-            __float2bfloat16_rn(broken || L == 0.f ? 0.f : O / L);
+        const int rr = r0g + hd, j = rr / p.G;
+        p.out[((static_cast<int64_t>(sq.row0) + j) * p.Hq + static_cast<int64_t>(kvh) * p.G + (rr - j * p.G)) * DH +
+              i % DH] = __float2bfloat16_rn(broken || L == 0.f ? 0.f : O / L);
       } else {
         p.ws_o[slot * C::kHeads * DH + i] = O;
         if (i % DH == 0) {
@@ -666,8 +705,9 @@ __global__ void __launch_bounds__(256) merge_paged_kernel(const PagedDecodeParam
   const int n = static_cast<int>(c1 - c0 + 1), total = n + (own >= 0 ? 1 : 0);
   if (total == 0) return;
   auto slot = [&](int i) { return i == n ? own : (c0 + i) * kDSlots + (i == 0 ? w0 : 0); };
-  const int kvh = hg / p.NG, head0 = kvh * p.G + (hg - kvh * p.NG) * kHeads;
-  const int nh = min(kHeads, (kvh + 1) * p.G - head0);
+  const int kvh = hg / p.NG, r0g = (hg - kvh * p.NG) * kHeads;
+  const DecSeq sq = dec_seq(p, b);
+  const int nh = min(kHeads, sq.n * p.G - r0g);
   for (int i = threadIdx.x; i < nh * DH / 4; i += 256) {
     const int hd = i / (DH / 4);
     float M = -INFINITY;
@@ -695,20 +735,22 @@ __global__ void __launch_bounds__(256) merge_paged_kernel(const PagedDecodeParam
     const float r = broken || L == 0.f ? 0.f : 1.f / L;
     const uint2 y = broken ? make_uint2(0u, 0u)
                            : make_uint2(pack_bf16x2(O.x * r, O.y * r), pack_bf16x2(O.z * r, O.w * r));
-    reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(b) * p.Hq + head0) * DH)[i] = y;
+    const int rr = r0g + hd, j = rr / p.G;
+    reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(sq.row0) + j) * p.Hq + static_cast<int64_t>(kvh) * p.G +
+                                      (rr - j * p.G)) * DH)[i - hd * (DH / 4)] = y;
   }
 }
 
 struct DecPlan {
-  int G, NT, NG, HG;
+  int NT, NG, HG;
   size_t o_bytes, ml_bytes, pre_bytes;
 };
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-DecPlan dec_plan(const slim_paged_cache& c, int Hq) {
+// R query rows at most share a (sequence, key head)'s keys.
+DecPlan dec_plan(const slim_paged_cache& c, int R) {
   DecPlan d;
-  d.G = Hq / c.Hkv;
-  d.NT = d.G > 8 ? 2 : 1;
-  d.NG = (d.G + 8 * d.NT - 1) / (8 * d.NT);
+  d.NT = R <= 8 ? 1 : R <= 16 ? 2 : 4;
+  d.NG = (R + 8 * d.NT - 1) / (8 * d.NT);
   d.HG = c.Hkv * d.NG;
   const size_t slots = static_cast<size_t>(num_sms()) * kDSlots;
   d.o_bytes = up256(slots * 8 * d.NT * c.dh * 4);
@@ -758,23 +800,37 @@ cudaError_t launch_dec(const PagedDecodeParams& p, cudaStream_t st, int* launche
 
 }  // namespace
 
-size_t paged_decode_ws_bytes(const slim_paged_cache& c, int Hq) {
-  const DecPlan d = dec_plan(c, Hq);
+size_t paged_rows_ws_bytes(const slim_paged_cache& c, int R) {
+  const DecPlan d = dec_plan(c, R);
   return d.o_bytes + d.ml_bytes + d.pre_bytes;
 }
 
-cudaError_t launch_paged_decode(const slim_paged_cache& c, const void* q, int64_t q_stride, const int32_t* lens,
-                                int rows_extra, int Hq, int64_t t_hint, void* out, void* workspace, int32_t* status,
-                                cudaStream_t st, int* launches) {
-  const DecPlan d = dec_plan(c, Hq);
+template <bool E, int DH>
+static cudaError_t launch_dec_nt(const PagedDecodeParams& p, int NT, cudaStream_t st, int* launches) {
+  return NT == 1   ? launch_dec<E, DH, 1>(p, st, launches)
+         : NT == 2 ? launch_dec<E, DH, 2>(p, st, launches)
+                   : launch_dec<E, DH, 4>(p, st, launches);
+}
+
+// starts == nullptr: one row per sequence, attending lens[b] + rows_extra keys; else the packed rows,
+// at most max_new of a sequence, each attending the keys up to its own.
+cudaError_t launch_paged_rows(const slim_paged_cache& c, const void* q, int64_t q_stride, const int32_t* starts,
+                              const int32_t* lens, int64_t rows, int64_t max_new, int rows_extra, int Hq,
+                              int64_t t_hint, void* out, void* workspace, int32_t* status, cudaStream_t st,
+                              int* launches) {
+  const int G = Hq / c.Hkv;
+  const DecPlan d = dec_plan(c, starts ? static_cast<int>(max_new) * G : G);
   PagedDecodeParams p;
   p.c = paged_view(c);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride = q_stride;
   p.lens = lens;
+  p.starts = starts;
+  p.rows = rows;
+  p.max_new = max_new;
   p.extra = rows_extra;
   p.Hq = Hq;
-  p.G = d.G;
+  p.G = G;
   p.NG = d.NG;
   p.HG = d.HG;
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -787,12 +843,9 @@ cudaError_t launch_paged_decode(const slim_paged_cache& c, const void* q, int64_
   const int64_t hint = t_hint > 0 ? std::min(t_hint, p.c.cap) : p.c.cap;
   // one CTA per work sequence, no merge, where that is one wave and a warp's share stays short
   p.split = !(static_cast<int64_t>(c.B) * d.HG <= num_sms() && hint <= 1024);
-  if (c.dtype == SLIM_E4M3) {
-    if (c.dh == 64) return d.NT == 1 ? launch_dec<true, 64, 1>(p, st, launches) : launch_dec<true, 64, 2>(p, st, launches);
-    return d.NT == 1 ? launch_dec<true, 128, 1>(p, st, launches) : launch_dec<true, 128, 2>(p, st, launches);
-  }
-  if (c.dh == 64) return d.NT == 1 ? launch_dec<false, 64, 1>(p, st, launches) : launch_dec<false, 64, 2>(p, st, launches);
-  return d.NT == 1 ? launch_dec<false, 128, 1>(p, st, launches) : launch_dec<false, 128, 2>(p, st, launches);
+  if (c.dtype == SLIM_E4M3)
+    return c.dh == 64 ? launch_dec_nt<true, 64>(p, d.NT, st, launches) : launch_dec_nt<true, 128>(p, d.NT, st, launches);
+  return c.dh == 64 ? launch_dec_nt<false, 64>(p, d.NT, st, launches) : launch_dec_nt<false, 128>(p, d.NT, st, launches);
 }
 
 }  // namespace slim

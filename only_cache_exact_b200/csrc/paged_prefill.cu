@@ -804,6 +804,11 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PagedPrefillPa
   for (int k = 0; k < PL; k += 2) dst[k / 2] = broken ? 0u : pack_bf16x2(o[k] * inv, o[k + 1] * inv);
 }
 
+// Rows of a (sequence, key head) up to which the kernel of paged_decode.cu is taken: it streams the
+// cache near memory speed, where a 128-row tile here would be mostly empty.
+constexpr int kFFewRows = 32;
+bool pf_few(const slim_paged_cache& c, int Hq, int64_t max_new) { return max_new * (Hq / c.Hkv) <= kFFewRows; }
+
 struct PfPlan {
   int G, QPT, pairs, splits;
   size_t o_bytes, ml_bytes;
@@ -859,11 +864,13 @@ cudaError_t launch_pf(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pa
 }  // namespace
 
 bool paged_prefill_fits(const slim_paged_cache& c, int Hq, int64_t rows, int64_t max_new, int64_t t_hint) {
+  if (pf_few(c, Hq, max_new)) return true;
   const PfPlan f = pf_plan(c, Hq, rows, max_new, t_hint);
   return static_cast<int64_t>(c.B) * c.Hkv * f.pairs * f.splits < (int64_t(1) << 31);
 }
 
 size_t paged_prefill_ws_bytes(const slim_paged_cache& c, int Hq, int64_t rows, int64_t max_new, int64_t t_hint) {
+  if (pf_few(c, Hq, max_new)) return paged_rows_ws_bytes(c, static_cast<int>(max_new) * (Hq / c.Hkv));
   const PfPlan f = pf_plan(c, Hq, rows, max_new, t_hint);
   return f.o_bytes + f.ml_bytes;
 }
@@ -871,6 +878,9 @@ size_t paged_prefill_ws_bytes(const slim_paged_cache& c, int Hq, int64_t rows, i
 cudaError_t launch_paged_prefill(const slim_paged_cache& c, const void* q, int64_t q_stride, const int32_t* starts,
                                  const int32_t* lens, int64_t rows, int64_t max_new, int Hq, int64_t t_hint,
                                  void* out, void* workspace, int32_t* status, cudaStream_t st, int* launches) {
+  if (pf_few(c, Hq, max_new))
+    return launch_paged_rows(c, q, q_stride, starts, lens, rows, max_new, 0, Hq, t_hint, out, workspace, status, st,
+                             launches);
   const PfPlan f = pf_plan(c, Hq, rows, max_new, t_hint);
   PagedPrefillParams p;
   p.c = paged_view(c);

@@ -117,11 +117,12 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st, int* 
 cudaError_t launch_paged_gather(const slim_paged_cache& c, const int32_t* starts, const int32_t* first, int64_t rows,
                                 int64_t max_new, void* k_out, void* v_out, int32_t* status, cudaStream_t st,
                                 int* launches);
-size_t paged_decode_ws_bytes(const slim_paged_cache& c, int Hq);
-cudaError_t launch_paged_decode(const slim_paged_cache& c, const void* q, int64_t q_stride, const int32_t* lens,
-                                int rows_extra, int Hq, int64_t t_hint, void* out, void* workspace, int32_t* status,
-                                cudaStream_t st, int* launches);
-
+// A few rows per (sequence, key head): R at most, packed (starts) or one row b for sequence b.
+size_t paged_rows_ws_bytes(const slim_paged_cache& c, int R);
+cudaError_t launch_paged_rows(const slim_paged_cache& c, const void* q, int64_t q_stride, const int32_t* starts,
+                              const int32_t* lens, int64_t rows, int64_t max_new, int rows_extra, int Hq,
+                              int64_t t_hint, void* out, void* workspace, int32_t* status, cudaStream_t st,
+                              int* launches);
 bool paged_prefill_fits(const slim_paged_cache& c, int Hq, int64_t rows, int64_t max_new, int64_t t_hint);
 size_t paged_prefill_ws_bytes(const slim_paged_cache& c, int Hq, int64_t rows, int64_t max_new, int64_t t_hint);
 cudaError_t launch_paged_prefill(const slim_paged_cache& c, const void* q, int64_t q_stride, const int32_t* starts,

@@ -105,6 +105,64 @@ def test_long_cache_few_rows(S, kind, dh, page, G):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dh,page,G", [(64, 16, 2), (128, 64, 4), (128, 128, 8)])
+def test_long_cache_short_chunks(S, kind, dh, page, G):
+    """More rows than the few-row kernel takes, keys split over CTAs and joined, among them splits that a short
+    sequence has nothing in."""
+    cached, new = [5000, 3, 2047], [21, 33, 1]
+    total = [a + n for a, n in zip(cached, new)]
+    st = PagedState(S, kind, 1, dh, page, total, total, seed=30)
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows(new, G, 2.0)
+    out = run(S, st, q, new, cached, max_new=33)
+    assert S.slim_last_launch_count() == 2 and int(st.status.item()) == 0
+    check(st, q, out, new, cached)
+    assert torch.equal(out, run(S, st, q, new, cached, max_new=33))
+    one = run(S, st, q, new, cached, max_new=33, t_hint=1)  # unsplit
+    assert S.slim_last_launch_count() == 1
+    check(st, q, one, new, cached)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,dh,page,new", [
+    (3, 3, 64, 16, [5, 0, 8, 1, 2]), (6, 3, 128, 32, [4, 1, 0, 3, 2]), (4, 2, 64, 64, [8, 7, 1, 5, 0]),
+    (4, 1, 128, 128, [4, 4, 4, 3, 1]), (8, 1, 64, 32, [1, 4, 3, 2, 4]), (32, 1, 128, 16, [1, 1, 0, 1, 1]),
+    (5, 1, 128, 64, [6, 1, 2, 0, 5]), (2, 2, 64, 128, [32, 17, 16, 1, 0])])
+@pytest.mark.parametrize("t_hint", [1, 0])
+def test_few_rows(S, kind, Hq, Hkv, dh, page, new, t_hint):
+    """Up to 32 rows (queries and heads) of a key head: each row has its own last key, among others inside a 16-key
+    tile and on either side of its border."""
+    cached = [0, 14, 700, 1500, 31]
+    total = [a + n for a, n in zip(cached, new)]
+    st = PagedState(S, kind, Hkv, dh, page, total, total, seed=31)
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows(new, Hq, 2.0)
+    out = run(S, st, q, new, cached, max_new=max(new), t_hint=t_hint)
+    assert int(st.status.item()) == 0
+    check(st, q, out, new, cached)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("t_hint", [1, 0])
+def test_few_rows_skipped(S, kind, t_hint):
+    """Bad lengths and pages with few rows: zeros for the sequence, or for the rows that reach the page."""
+    cached, new = [3, 9, 45, 700], [4, 4, 5, 2]
+    total = [a + n for a, n in zip(cached, new)]
+    st = PagedState(S, kind, 2, 64, 16, total, total, seed=32)
+    cap = st.cache.cap
+    st.table[2, 3] = -1      # positions 48..63
+    st.table[3, 7] = 1 << 30
+    lens = torch.tensor([-1, cap - 2, 45, 700], dtype=torch.int32, device="cuda")
+    q = st.rows(new, 4)
+    out = run(S, st, q, new, cached, max_new=5, t_hint=t_hint, lens=lens)
+    assert int(st.status.item()) == S.SLIM_DEV_BADLEN | S.SLIM_DEV_OVERFLOW | S.SLIM_DEV_BADPAGE
+    assert (out[:8] == 0).all() and (out[11:] == 0).all()
+    K, V = (st.oracle[w].read(st.table_h[2], 48) for w in (0, 1))
+    o, A, D = P.attend(f64(q[8:11]), K, V, [45, 46, 47])
+    assert (np.abs(f64(out[8:11]) - o) <= bound(kind, 64, o, A, D)).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_agrees_with_decode(S, kind):
     """One new row per sequence: the two forms of the attention agree within their tolerances."""
     cached = [0, 100, 1500]
