@@ -79,14 +79,25 @@ __device__ __forceinline__ float scale_log2(float s) {
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
-// Two e4m3 codes as an f16 pair (exact: f16 holds every e4m3 value).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// e4m3 codes as f16 pairs (exact: f16 holds every e4m3 value); lo from the low two bytes, hi from the
+// high two. In PTX so that each pair is one instruction, without the moves that put the CUDA
+// function's two halves together again.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
-  const uint32_t h = e4m3x2_to_f16x2(codes);
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Two floats rounded to a bf16 or f16 pair, lo in the low half: one instruction.
+__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t round_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Host: the view of a checked cache.

@@ -91,7 +91,7 @@ __device__ __forceinline__ void load_unit(const __nv_bfloat16* src, int e0, int 
 }
 
 __device__ __forceinline__ uint4 pack8_bf16(const float* x) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  return make_uint4(round_bf16x2(x[0], x[1]), round_bf16x2(x[2], x[3]), round_bf16x2(x[4], x[5]), round_bf16x2(x[6], x[7]));
 }
 // Codes of 8 values; zeros under a NaN scale, so that only the scale carries it.
 __device__ __forceinline__ uint2 pack8_e4m3(const float* x, float inv) {
@@ -107,7 +107,9 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, float ratio) {
   uint32_t in[4] = {w.x, w.y, w.z, w.w}, out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 a = e4m3x2_to_float2(in[i] & 0xffffu), b = e4m3x2_to_float2(in[i] >> 16);
+    uint32_t lo, hi;
+    e4m3x4_to_f16(in[i], lo, hi);
+    const float2 a = f16x2_to_float2(lo), b = f16x2_to_float2(hi);
     out[i] = to_e4m3x2(a.x * ratio, a.y * ratio) | (to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
@@ -389,9 +391,11 @@ __global__ void __launch_bounds__(kAppThreads) gather_kernel(const GatherParams 
         uint32_t y[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 a = e4m3x2_to_float2(w[e] & 0xffffu), c = e4m3x2_to_float2(w[e] >> 16);
-          y[2 * e] = pack_bf16x2(a.x * s, a.y * s);
-          y[2 * e + 1] = pack_bf16x2(c.x * s, c.y * s);
+          uint32_t lo, hi;
+          e4m3x4_to_f16(w[e], lo, hi);
+          const float2 a = f16x2_to_float2(lo), c = f16x2_to_float2(hi);
+          y[2 * e] = round_bf16x2(a.x * s, a.y * s);
+          y[2 * e + 1] = round_bf16x2(c.x * s, c.y * s);
         }
         o0 = make_uint4(y[0], y[1], y[2], y[3]);
         o1 = make_uint4(y[4], y[5], y[6], y[7]);

@@ -38,10 +38,9 @@ namespace slim {
 
 namespace {
 
-constexpr int kDW = 8;                 // warps of a CTA
-constexpr int kDThreads = kDW * 32;
-constexpr int kDRing = 24 * 1024;      // bytes of a warp's ring
-constexpr int kDSlots = 2 * kDW;       // partials a CTA can leave: kDW of warps' ends, kDW of sequences that end inside a warp's share
+constexpr int kDRings = 192 * 1024;    // bytes of a CTA's rings
+constexpr int kDMergeScan = 256;       // up to this many sequences the merge kernel takes the line's offsets from lens itself
+constexpr float kDLazyLog2 = 8.f;      // a row's maximum follows once a score exceeds it by this much
 
 struct PagedDecodeParams {
   PagedView c;
@@ -54,8 +53,8 @@ struct PagedDecodeParams {
   int Hq, G, NG;  // G query heads per key head; rows of a (sequence, key head) in NG groups
   int HG;         // Hkv * NG work sequences per cache sequence
   __nv_bfloat16* out;
-  float* ws_o;     // [ctas][kDSlots][heads][dh]
-  float* ws_ml;    // [ctas][kDSlots][heads][2]
+  float* ws_o;     // [ctas][kSlots][rows][dh]
+  float* ws_ml;    // [ctas][kSlots][rows][2]
   uint32_t* ws_pre;  // [B + 1] tiles before each sequence
   int32_t* status;
   int split;
@@ -102,11 +101,6 @@ __device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // A sequence's query rows and keys. Row j (of n) sits at position len + j - n and attends the keys
 // up to its own; keys is 0 where there is nothing to do or the sequence is skipped (bits says why).
 struct DecSeq {
@@ -135,29 +129,52 @@ __device__ __forceinline__ DecSeq dec_seq(const PagedDecodeParams& p, int b) {
   return s;
 }
 
-// CTA c of A owns line tiles [c·X/A, (c+1)·X/A); inside it warp w owns `chunk` tiles from w·chunk.
-__device__ __forceinline__ int64_t cta_start(int64_t c, int64_t X, int64_t A) { return c * X / A; }
-__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t X, int64_t A) { return ((x + 1) * A - 1) / X; }
-__device__ __forceinline__ int64_t active_ctas(int64_t X, int64_t grid) {
-  return max(int64_t(1), min(grid, X / kDW));
+#ifndef DEC_B64
+#define DEC_B64 8
+#define DEC_B128 8
+#endif
+__host__ __device__ constexpr int dec_warps(bool e4m3, int dh, int NT) {
+  return NT > 1 ? 8 : e4m3 ? (dh == 64 ? 16 : 12) : dh == 64 ? DEC_B64 : DEC_B128;
 }
+
+// The line has X tiles. CTA c of A owns [c·X/A, (c+1)·X/A), its warp w `chunk` tiles from w·chunk on.
+// I is int where c·X fits (64-bit divisions took 0.5 us of a call), int64_t else.
+template <typename I>
+__device__ __forceinline__ I active_ctas(I X, I grid, int warps) {
+  return max(I(1), min(grid, X / warps));
+}
+template <typename I, int W>
+__device__ __forceinline__ void warp_share(I X, I grid, int cta, int warp, I& x, int& left) {
+  const I A = active_ctas<I>(X, grid, W);
+  x = 0;
+  left = 0;
+  if (cta >= A) return;
+  const I c0 = cta * X / A, c1 = (cta + 1) * X / A, chunk = (c1 - c0 + W - 1) / W;
+  x = c0 + warp * chunk;
+  left = static_cast<int>(min(chunk, c1 - x));
+}
+__device__ __forceinline__ bool line_fits_int(int64_t X, int grid) { return X < ((int64_t(1) << 31) - 1) / (grid + 1); }
 
 // A stretch of tiles of one (sequence, head group).
 struct DecSeg {
   int b, hg, T;      // T tiles in the whole sequence
   int tile, end;     // [tile, end)
 };
+// A warp's partial at the end of its share: its stretch, and the sequence's query rows.
+struct DecEnd {
+  DecSeg s;
+  int row0, n;
+};
 // Walks the line from a starting point over `left` tiles.
 struct DecCursor {
-  int b, hg, tile, T;
-  int64_t left;
+  int b, hg, tile, T, left;
   __device__ __forceinline__ bool next(DecSeg& s, const uint32_t* pre, int HG) {
     if (left <= 0) return false;
     s.b = b;
     s.hg = hg;
     s.T = T;
     s.tile = tile;
-    const int n = static_cast<int>(min(static_cast<int64_t>(T - tile), left));
+    const int n = min(T - tile, left);
     s.end = tile + n;
     left -= n;
     tile = 0;
@@ -174,14 +191,19 @@ struct DecCursor {
 
 template <bool E, int DH, int NT>
 struct DecCfg {
+  static constexpr int kWarps = dec_warps(E, DH, NT);
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRing = kDRings / kWarps;           // bytes of a warp's ring
+  // partials a CTA can leave: of its warps' ends, and of sequences that end inside a warp's share
+  static constexpr int kSlots = 2 * kWarps;
   static constexpr int kRowB = DH * (E ? 1 : 2);           // bytes of a row
   static constexpr int kTileB = 16 * kRowB;                // K (or V) of a tile
   static constexpr int kTT = kTileB >= 4096 || NT == 4 ? 1 : 2;  // tiles of a stage (32 rows: registers)
   static constexpr int kStageB = 2 * kTT * kTileB;
-  static constexpr int kStages = kDRing / kStageB;
+  static constexpr int kStages = kRing / kStageB;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kPartB = kHeads * DH * 4;           // a partial's O in the ring
-  static_assert(kPartB <= kDRing, "a partial fits the warp's ring");
+  static_assert(kPartB <= kRing, "a partial fits the warp's ring");
   // byte offset of 16-byte chunk c of row r: eight rows at one chunk (an ldmatrix phase) meet eight
   // different 16-byte banks
   __device__ static __forceinline__ uint32_t at(int r, int c) {
@@ -190,24 +212,25 @@ struct DecCfg {
 };
 
 template <bool E, int DH, int NT>
-__global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedDecodeParams p) {
+__global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_kernel(const PagedDecodeParams p) {
   using C = DecCfg<E, DH, NT>;
   extern __shared__ __align__(128) uint8_t dec_smem[];
-  float* s_scale = reinterpret_cast<float*>(dec_smem + kDW * kDRing);  // [warp][stage][tile][k, v]
-  float* s_ml = s_scale + kDW * C::kStages * C::kTT * 2;               // [warp][head][m, l]
-  int64_t* s_seq = reinterpret_cast<int64_t*>(s_ml + kDW * C::kHeads * 2);  // [warp] sequence of its end partial, -1: none
-  int* s_seg = reinterpret_cast<int*>(s_seq + kDW);                    // [warp][tile, end, T]
-  uint32_t* s_pre = reinterpret_cast<uint32_t*>(s_seg + kDW * 4);      // [B + 1]
+  float* s_scale = reinterpret_cast<float*>(dec_smem + C::kWarps * C::kRing);  // [warp][stage][tile][k, v]
+  float* s_ml = s_scale + C::kWarps * C::kStages * C::kTT * 2;               // [warp][head][m, l]
+  DecEnd* s_end = reinterpret_cast<DecEnd*>(s_ml + C::kWarps * C::kHeads * 2);  // [warp] its end partial, b = -1: none
+  uint32_t* s_pre = reinterpret_cast<uint32_t*>(s_end + C::kWarps);             // [B + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lg = lane >> 2, lq = lane & 3;
-  pdl_launch_dependents();
+  // the merge kernel may start once every CTA is past this wait: what came before is complete then,
+  // so that it may read lens and starts at once
   pdl_wait_primary();
+  pdl_launch_dependents();
 
   // ---------------------------------------------------------------- this warp's share
   auto zero_rows = [&](const DecSeq& q) {
     if (!q.span) return;
     const int64_t n = static_cast<int64_t>(q.n) * p.Hq * DH / 8;
-    for (int64_t i = threadIdx.x; i < n; i += kDThreads)
+    for (int64_t i = threadIdx.x; i < n; i += C::kThreads)
       reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(q.row0) * p.Hq * DH)[i] = make_uint4(0u, 0u, 0u, 0u);
   };
   DecCursor cur;
@@ -237,18 +260,22 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
       if (blockIdx.x == 0 && lane == 0 && bits) atomicOr(p.status, bits);
     }
     __syncthreads();
-    if (blockIdx.x == 0)
-      for (int b = threadIdx.x; b <= p.c.B; b += kDThreads) p.ws_pre[b] = s_pre[b];
+    if (blockIdx.x == 0 && p.c.B > kDMergeScan)
+      for (int b = threadIdx.x; b <= p.c.B; b += C::kThreads) p.ws_pre[b] = s_pre[b];
     const int64_t X = static_cast<int64_t>(s_pre[p.c.B]) * p.HG;
-    const int64_t A = active_ctas(X, gridDim.x);
+    const int grid = static_cast<int>(gridDim.x);
     cur.left = 0;
-    if (X > 0 && blockIdx.x < A) {
-      const int64_t c0 = cta_start(blockIdx.x, X, A), c1 = cta_start(blockIdx.x + 1, X, A);
-      const int64_t chunk = (c1 - c0 + kDW - 1) / kDW;
-      const int64_t x = c0 + warp * chunk;
-      cur.left = min(chunk, c1 - x);
+    if (X > 0) {
+      int64_t x;
+      if (line_fits_int(X, grid)) {
+        int xi;
+        warp_share<int, C::kWarps>(static_cast<int>(X), grid, blockIdx.x, warp, xi, cur.left);
+        x = xi;
+      } else {
+        warp_share<int64_t, C::kWarps>(X, grid, blockIdx.x, warp, x, cur.left);
+      }
       if (cur.left > 0) {
-        int lo = 0, hi = p.c.B;  // the last b with s_pre[b]·HG <= x that has tiles
+        int lo = 0, hi = p.c.B;  // the last b with s_pre[b]·HG <= x: it has tiles
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
           if (static_cast<int64_t>(s_pre[mid]) * p.HG <= x) lo = mid; else hi = mid;
@@ -256,7 +283,7 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
         cur.b = lo;
         cur.T = static_cast<int>(s_pre[lo + 1] - s_pre[lo]);
         const int64_t rem = x - static_cast<int64_t>(s_pre[lo]) * p.HG;
-        cur.hg = static_cast<int>(rem / cur.T);
+        cur.hg = rem < (int64_t(1) << 31) ? static_cast<int>(rem) / cur.T : static_cast<int>(rem / cur.T);
         cur.tile = static_cast<int>(rem - static_cast<int64_t>(cur.hg) * cur.T);
       }
     }
@@ -269,13 +296,13 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
     const DecSeq q = dec_seq(p, cur.b);
     cur.T = (q.keys + 15) >> 4;
     if (q.bits && cur.hg == 0 && threadIdx.x == 0) atomicOr(p.status, q.bits);
-    const int chunk = (cur.T + kDW - 1) / kDW;
+    const int chunk = (cur.T + C::kWarps - 1) / C::kWarps;
     cur.tile = warp * chunk;
     cur.left = min(chunk, cur.T - cur.tile);
     if (cur.T == 0 && cur.hg == 0) zero_rows(q);
   }
 
-  uint8_t* ring = dec_smem + warp * kDRing;
+  uint8_t* ring = dec_smem + warp * C::kRing;
   const uint32_t ring_u = smem_u32(ring);
   float* my_scale = s_scale + warp * C::kStages * C::kTT * 2;
 
@@ -345,7 +372,7 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
   for (int s = 0; s < C::kStages - 1; ++s) issue(s);
 
   // ---------------------------------------------------------------- compute
-  if (lane == 0) s_seq[warp] = -1;
+  if (lane == 0) s_end[warp].s.b = -1;
   DecSeg sg;
   int stage = 0;
   while (cur.next(sg, s_pre, p.HG)) {
@@ -381,8 +408,8 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
         const float inv = exp2_int(-e), f = exp2_int(e) * p.scale_log2;
 #pragma unroll
         for (int j = 0; j < DH / 16; ++j) {
-          qf[n][j][0] = pack_f16x2(bf16lo(w[j].x) * inv, bf16hi(w[j].x) * inv);
-          qf[n][j][1] = pack_f16x2(bf16lo(w[j].y) * inv, bf16hi(w[j].y) * inv);
+          qf[n][j][0] = round_f16x2(bf16lo(w[j].x) * inv, bf16hi(w[j].x) * inv);
+          qf[n][j][1] = round_f16x2(bf16lo(w[j].y) * inv, bf16hi(w[j].y) * inv);
         }
         hs[n][0] = __shfl_sync(0xffffffffu, f, lq * 8);
         hs[n][1] = __shfl_sync(0xffffffffu, f, lq * 8 + 4);
@@ -396,15 +423,18 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
       }
     }
     float o[DH / 16][NT][4] = {};
-    float m[NT][2], l[NT][2];
+    float m[NT][2], neg_m[NT][2], l[NT][2];  // neg_m: -m, 0 while there is none
 #pragma unroll
-    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+    for (int n = 0; n < NT; ++n)
+      m[n][0] = m[n][1] = -INFINITY, neg_m[n][0] = neg_m[n][1] = 0.f, l[n][0] = l[n][1] = 0.f;
     int bad_pos = 0x7fffffff;  // first key of the segment whose page is outside the pool
     int lim[NT][2];            // keys that rows 2 lq and 2 lq + 1 attend
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) lim[n][i] = sq.keys - sq.n + 1 + min(r0g + n * 8 + 2 * lq + i, sq.n * p.G - 1) / p.G;
+
+    const int lim_all = sq.keys - sq.n + 1 + r0g / p.G;  // keys that every row of the group attends
 
     for (int t = sg.tile; t < sg.end; t += C::kTT) {
       cp_async_wait<C::kStages - 2>();
@@ -429,8 +459,9 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
               ldsm4(base + C::at((lane & 7) + ((lane >> 3) & 1) * 8, j + (lane >> 4)), r);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * i] & 0xffffu), e4m3x2_to_f16x2(r[2 * i + 1] & 0xffffu),
-                                       e4m3x2_to_f16x2(r[2 * i] >> 16), e4m3x2_to_f16x2(r[2 * i + 1] >> 16)};
+                uint32_t a[4];
+                e4m3x4_to_f16(r[2 * i], a[0], a[2]);
+                e4m3x4_to_f16(r[2 * i + 1], a[1], a[3]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) mma_16816_f16(s[k][n], a, qf[n][j + i][0], qf[n][j + i][1]);
               }
@@ -446,51 +477,65 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
           }
         }
       }
-      // scores in log2 units, rows past the length masked; rows lg and lg + 8 of the tile
-      float mx[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-      float lv[C::kTT];
+      // Exponent of a weight: s·f + add, f the factor to log2 units, add = lv - m. Tiles that some row
+      // does not attend whole (the last ones) are scaled and masked here, with f = 1 from then on.
+      float f[C::kTT][NT][2], lv[C::kTT], fac[C::kTT];
+      const bool full = (t + C::kTT) * 16 <= lim_all && tiles == C::kTT;
 #pragma unroll
       for (int k = 0; k < C::kTT; ++k) {
         const float ks = E && k < tiles ? my_scale[(stage * C::kTT + k) * 2] : 1.f;
         lv[k] = E && k < tiles ? scale_log2(my_scale[(stage * C::kTT + k) * 2 + 1]) : 0.f;
-        const int r0 = (t + k) * 16 + lg;
+        fac[k] = E ? ex2(-lv[k]) : 1.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float f = E ? hs[n][i & 1] * ks : hs[n][i & 1];
-            s[k][n][i] = k < tiles && r0 + (i >> 1) * 8 < lim[n][i & 1] ? s[k][n][i] * f : -INFINITY;
-            mx[n][i & 1] = fmaxf(mx[n][i & 1], E ? s[k][n][i] + lv[k] : s[k][n][i]);
-          }
-        }
+          for (int i = 0; i < 2; ++i) f[k][n][i] = E ? hs[n][i] * ks : hs[n][i];
       }
-      bool same = true;
-      float alpha[NT][2];
+      if (!full) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+        for (int k = 0; k < C::kTT; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              s[k][n][i] = k < tiles && (t + k) * 16 + lg + (i >> 1) * 8 < lim[n][i & 1] ? s[k][n][i] * f[k][n][i & 1]
+                                                                                        : -INFINITY;
+            f[k][n][0] = f[k][n][1] = 1.f;
+          }
+      }
+      // A lane looks at its own scores only; the warp's maximum is taken when one of them exceeds the
+      // row's by more than 2^8 (weights up to that are harmless in f16 and bf16).
+      float mx[NT][2];
+      bool grow = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float x = mx[n][i];
+          mx[n][i] = -INFINITY;
 #pragma unroll
-          for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
-          const float mn = fmaxf(m[n][i], x);
-          alpha[n][i] = mn == -INFINITY ? 1.f : ex2(m[n][i] - mn);
-          m[n][i] = mn;
-          l[n][i] *= alpha[n][i];
-          same = same && alpha[n][i] == 1.f;
+          for (int k = 0; k < C::kTT; ++k)
+            mx[n][i] = fmaxf(mx[n][i], fmaf(fmaxf(s[k][n][i], s[k][n][i + 2]), f[k][n][i], lv[k]));
+          grow = grow || mx[n][i] > m[n][i] + kDLazyLog2;
         }
-      }
-      if (!__all_sync(0xffffffffu, same)) {
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < DH / 16; ++c) {
+          for (int i = 0; i < 2; ++i) {
+            float x = mx[n][i];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[c][n][i] *= alpha[n][i & 1];
+            for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
+            const float mn = fmaxf(m[n][i], x);
+            const float alpha = mn == -INFINITY ? 1.f : ex2(m[n][i] - mn);
+            m[n][i] = mn;
+            neg_m[n][i] = mn == -INFINITY ? 0.f : -mn;
+            l[n][i] *= alpha;
+#pragma unroll
+            for (int c = 0; c < DH / 16; ++c) {
+              o[c][n][i] *= alpha;
+              o[c][n][i + 2] *= alpha;
+            }
           }
-        }
       }
 #pragma unroll
       for (int k = 0; k < C::kTT; ++k) {
@@ -499,27 +544,42 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float e[4];
+          bool low = false;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float mm = m[n][i] == -INFINITY ? 0.f : m[n][i];
-            float add = lv[k] - mm;
-            if (E) {  // weights below 2^-60 are zero in f16; raised, their fp32 sum does not underflow
-              const float top = fmaxf(s[k][n][i], s[k][n][i + 2]);
-              if (top != -INFINITY && add < -60.f - top) add = -60.f - top;  // a NaN scale stays
+            const float add = lv[k] + neg_m[n][i];
+            float x0 = fmaf(s[k][n][i], f[k][n][i], add), x1 = fmaf(s[k][n][i + 2], f[k][n][i], add);
+            if (E && !full) {  // a masked weight is zero also beside a NaN scale
+              if (s[k][n][i] == -INFINITY) x0 = -INFINITY;
+              if (s[k][n][i + 2] == -INFINITY) x1 = -INFINITY;
             }
-            e[i] = ex2(s[k][n][i] + add);
-            e[i + 2] = ex2(s[k][n][i + 2] + add);
-            l[n][i] += E ? (e[i] + e[i + 2]) * ex2(-mm - add) : e[i] + e[i + 2];
+            e[i] = ex2(x0);
+            e[i + 2] = ex2(x1);
+            if (!E) l[n][i] += e[i] + e[i + 2];
+            if (E) low = low || fminf(x0, x1) < -60.f;
           }
           if (E) {
-            ph[n][0] = movmatrix(pack_f16x2(e[0], e[1]));
-            ph[n][1] = movmatrix(pack_f16x2(e[2], e[3]));
+            // the sum of p itself is that of P·2^-lv; taken from the scores where P may have underflowed
+            if (__any_sync(0xffffffffu, low)) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float z = fac[k] != fac[k] ? fac[k] : 0.f;  // a NaN scale stays
+                l[n][i] += ex2(fmaf(s[k][n][i], f[k][n][i], neg_m[n][i])) +
+                           ex2(fmaf(s[k][n][i + 2], f[k][n][i], neg_m[n][i])) + (e[i] != 0.f ? e[i] * z : 0.f) +
+                           (e[i + 2] != 0.f ? e[i + 2] * z : 0.f);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) l[n][i] = fmaf(e[i] + e[i + 2], fac[k], l[n][i]);
+            }
+            ph[n][0] = movmatrix(round_f16x2(e[0], e[1]));
+            ph[n][1] = movmatrix(round_f16x2(e[2], e[3]));
           } else {
-            const uint32_t h0 = pack_bf16x2(e[0], e[1]), h1 = pack_bf16x2(e[2], e[3]);
+            const uint32_t h0 = round_bf16x2(e[0], e[1]), h1 = round_bf16x2(e[2], e[3]);
             ph[n][0] = movmatrix(h0);
             ph[n][1] = movmatrix(h1);
-            pl[n][0] = movmatrix(pack_bf16x2(e[0] - bf16lo(h0), e[1] - bf16hi(h0)));
-            pl[n][1] = movmatrix(pack_bf16x2(e[2] - bf16lo(h1), e[3] - bf16hi(h1)));
+            pl[n][0] = movmatrix(round_bf16x2(e[0] - bf16lo(h0), e[1] - bf16hi(h0)));
+            pl[n][1] = movmatrix(round_bf16x2(e[2] - bf16lo(h1), e[3] - bf16hi(h1)));
           }
         }
         const uint32_t base = kb + k * 2 * C::kTileB + C::kTileB;
@@ -532,9 +592,9 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
             ldsm4_trans(base + C::at((lane & 7) + ((lane >> 3) & 1) * 8, j + (lane >> 4)), r);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t x = __byte_perm(r[2 * i], 0u, 0x3120), y = __byte_perm(r[2 * i + 1], 0u, 0x3120);
-              const uint32_t a[4] = {e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
-                                     e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16)};
+              uint32_t a[4];
+              e4m3x4_to_f16(__byte_perm(r[2 * i], 0u, 0x3120), a[0], a[1]);
+              e4m3x4_to_f16(__byte_perm(r[2 * i + 1], 0u, 0x3120), a[2], a[3]);
 #pragma unroll
               for (int n = 0; n < NT; ++n) mma_16816_f16(o[j + i][n], a, ph[n][0], ph[n][1]);
             }
@@ -586,7 +646,7 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
     } else {
       // a partial: in the ring where it is the warp's last segment (every load has landed by then),
       // else in the workspace
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) * kDSlots + kDW + warp;
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * C::kSlots + C::kWarps + warp;
       if (last) {
         cp_async_wait<0>();
         __syncwarp();
@@ -608,133 +668,147 @@ __global__ void __launch_bounds__(kDThreads, 1) paged_decode_kernel(const PagedD
             pm[hd * 2 + 1] = l[n][i];
           }
         }
-      if (last && lane == 0) {
-        s_seq[warp] = static_cast<int64_t>(sg.b) * p.HG + sg.hg;
-        s_seg[warp * 4] = sg.tile;
-        s_seg[warp * 4 + 1] = sg.end;
-        s_seg[warp * 4 + 2] = sg.T;
-      }
+      if (last && lane == 0) s_end[warp] = DecEnd{sg, sq.row0, sq.n};
     }
   }
   cp_async_wait<0>();
   __syncthreads();
 
   // ---------------------------------------------------------------- joining the warps' last partials
-  for (int w0 = 0; w0 < kDW;) {
-    const int64_t seq = s_seq[w0];
-    int w1 = w0 + 1;
-    if (seq < 0) {
-      w0 = w1;
-      continue;
+  // The warps [w0, w1) that end in one sequence share its rows; every group is joined at once.
+  const int b = s_end[warp].s.b, hg = s_end[warp].s.hg;
+  if (b < 0) return;
+  auto same = [&](int w) { return s_end[w].s.b == b && s_end[w].s.hg == hg; };
+  int w0 = warp, w1 = warp + 1;
+  while (w0 > 0 && same(w0 - 1)) --w0;
+  while (w1 < C::kWarps && same(w1)) ++w1;
+  const bool whole = s_end[w0].s.tile == 0 && s_end[w1 - 1].s.end == s_end[w0].s.T;
+  const int row0 = s_end[warp].row0;
+  const int kvh = hg / p.NG, r0g = (hg - kvh * p.NG) * C::kHeads;
+  const int nh = min(C::kHeads, s_end[warp].n * p.G - r0g);
+  const int64_t slot = static_cast<int64_t>(blockIdx.x) * C::kSlots + w0;
+  for (int hd = warp - w0; hd < nh; hd += w1 - w0) {
+    float M = -INFINITY, L = 0.f;
+    bool broken = false;
+    for (int w = w0; w < w1; ++w) M = fmaxf(M, s_ml[(w * C::kHeads + hd) * 2]);
+    const float Mf = M == -INFINITY ? 0.f : M;
+    constexpr int PL = DH / 32;  // columns of a lane
+    float O[PL] = {};
+    for (int w = w0; w < w1; ++w) {
+      const float f = ex2(s_ml[(w * C::kHeads + hd) * 2] - Mf), lw = s_ml[(w * C::kHeads + hd) * 2 + 1];
+      broken |= lw < 0.f;
+      L = fmaf(f, lw, L);
+      const float* src = reinterpret_cast<const float*>(dec_smem + w * C::kRing) + hd * DH + lane * PL;
+#pragma unroll
+      for (int k = 0; k < PL; ++k) O[k] = fmaf(f, src[k], O[k]);
     }
-    while (w1 < kDW && s_seq[w1] == seq) ++w1;
-    const bool whole = s_seg[w0 * 4] == 0 && s_seg[(w1 - 1) * 4 + 1] == s_seg[w0 * 4 + 2];
-    const int b = static_cast<int>(seq / p.HG), hg = static_cast<int>(seq - static_cast<int64_t>(b) * p.HG);
-    const int kvh = hg / p.NG, r0g = (hg - kvh * p.NG) * C::kHeads;
-    const DecSeq sq = dec_seq(p, b);
-    const int nh = min(C::kHeads, sq.n * p.G - r0g);
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) * kDSlots + w0;
-    for (int i = threadIdx.x; i < nh * DH; i += kDThreads) {
-      const int hd = i / DH;
-      float M = -INFINITY, L = 0.f, O = 0.f;
-      bool broken = false;
-      for (int w = w0; w < w1; ++w) M = fmaxf(M, s_ml[(w * C::kHeads + hd) * 2]);
-      const float Mf = M == -INFINITY ? 0.f : M;
-      for (int w = w0; w < w1; ++w) {
-        const float f = ex2(s_ml[(w * C::kHeads + hd) * 2] - Mf), lw = s_ml[(w * C::kHeads + hd) * 2 + 1];
-        broken |= lw < 0.f;
-        L = fmaf(f, lw, L);
-        O = fmaf(f, reinterpret_cast<const float*>(dec_smem + w * kDRing)[i], O);
-      }
-      if (whole) {
-        const int rr = r0g + hd, j = rr / p.G;
-        p.out[((static_cast<int64_t>(sq.row0) + j) * p.Hq + static_cast<int64_t>(kvh) * p.G + (rr - j * p.G)) * DH +
-              i % DH] = __float2bfloat16_rn(broken || L == 0.f ? 0.f : O / L);
-      } else {
-        p.ws_o[slot * C::kHeads * DH + i] = O;
-        if (i % DH == 0) {
-          p.ws_ml[(slot * C::kHeads + hd) * 2] = M;
-          p.ws_ml[(slot * C::kHeads + hd) * 2 + 1] = broken ? -1.f : L;
-        }
+    if (whole) {
+      const int rr = r0g + hd, j = rr / p.G;
+      const float r = broken || L == 0.f ? 0.f : 1.f / L;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(
+          p.out + ((static_cast<int64_t>(row0) + j) * p.Hq + static_cast<int64_t>(kvh) * p.G + (rr - j * p.G)) * DH +
+          lane * PL);
+#pragma unroll
+      for (int k = 0; k < PL; k += 2) dst[k / 2] = broken ? 0u : round_bf16x2(O[k] * r, O[k + 1] * r);
+    } else {
+      float* dst = p.ws_o + (slot * C::kHeads + hd) * DH + lane * PL;
+#pragma unroll
+      for (int k = 0; k < PL; k += 2) *reinterpret_cast<float2*>(dst + k) = make_float2(O[k], O[k + 1]);
+      if (lane == 0) {
+        p.ws_ml[(slot * C::kHeads + hd) * 2] = M;
+        p.ws_ml[(slot * C::kHeads + hd) * 2 + 1] = broken ? -1.f : L;
       }
     }
-    w0 = w1;
   }
 }
 
+// Slots that hold the partials of line stretch [x0, x1): joined ones of CTAs c0 .. c0+n-1 (of warp w0 in
+// the first, of warp 0 in the others), then `own`, a warp's, or -1. None: written whole by the split kernel.
+struct DecSlots {
+  int c0, n, w0, own;
+};
+template <typename I, int W>
+__device__ __forceinline__ DecSlots dec_slots(I x0, I x1, I X, I grid) {
+  const I A = active_ctas<I>(X, grid, W);
+  auto start = [&](I c) { return c * X / A; };
+  const I c0 = ((x0 + 1) * A - 1) / X, c1 = (x1 * A - 1) / X;
+  const I s0 = start(c0), e0 = start(c0 + 1), s1 = c1 == c0 ? s0 : start(c1), e1 = c1 == c0 ? e0 : start(c1 + 1);
+  const I k0 = (e0 - s0 + W - 1) / W, k1 = c1 == c0 ? k0 : (e1 - s1 + W - 1) / W;  // tiles of a warp
+  const I w0 = (x0 - s0) / k0, w1 = (x1 - 1 - s1) / k1;
+  const bool inside = x1 < min(s1 + (w1 + 1) * k1, e1);   // it ends inside the share of warp w1 ..
+  const bool own = inside && !(c0 == c1 && w0 == w1);     // .. with a slot of its own there
+  const bool joined = !inside || w1 > (c0 == c1 ? w0 : I(0));  // CTA c1 has a joined slot
+  DecSlots s;
+  s.c0 = static_cast<int>(c0);
+  s.w0 = static_cast<int>(w0);
+  s.own = own ? static_cast<int>(c1) * 2 * W + W + static_cast<int>(w1) : -1;
+  s.n = c0 == c1 && !own ? 0 : static_cast<int>(c1 - c0) + (joined ? 1 : 0);
+  return s;
+}
+
 // Joins the partials of one (sequence, head group) that more than one CTA (or a CTA's join and a
-// warp in whose share it ends) holds. Which slots those are follows from the plan alone.
-template <int DH, int NT>
-__global__ void __launch_bounds__(256) merge_paged_kernel(const PagedDecodeParams p, int64_t grid) {
+// warp in whose share it ends) holds. Which slots those are follows from the plan alone; the loads of
+// a slot's maximum, sum and output go out together.
+template <int DH, int NT, int W>
+__global__ void __launch_bounds__(256) merge_paged_kernel(const PagedDecodeParams p, int grid) {
   constexpr int kHeads = 8 * NT;
-  __shared__ int64_t s_range[4];
   pdl_launch_dependents();
-  pdl_wait_primary();
   const int b = blockIdx.x / p.HG, hg = blockIdx.x - b * p.HG;
-  if (threadIdx.x == 0) {
-    const int64_t q0 = __ldcg(p.ws_pre + b), q1 = __ldcg(p.ws_pre + b + 1);
-    const int64_t X = static_cast<int64_t>(__ldcg(p.ws_pre + p.c.B)) * p.HG;
-    const int64_t T = q1 - q0, x0 = q0 * p.HG + hg * T, x1 = x0 + T;
-    s_range[0] = 0;
-    s_range[1] = -1;
-    s_range[2] = 0;
-    s_range[3] = -1;
-    if (T > 0) {
-      const int64_t A = active_ctas(X, grid);
-      const int64_t c0 = cta_of(x0, X, A), c1 = cta_of(x1 - 1, X, A);
-      auto chunk_of = [&](int64_t c) {
-        return (cta_start(c + 1, X, A) - cta_start(c, X, A) + kDW - 1) / kDW;
-      };
-      const int64_t s0 = cta_start(c0, X, A), s1 = cta_start(c1, X, A), e1 = cta_start(c1 + 1, X, A);
-      const int64_t w0 = (x0 - s0) / chunk_of(c0), w1 = (x1 - 1 - s1) / chunk_of(c1);
-      const int64_t end_w1 = min(s1 + (w1 + 1) * chunk_of(c1), e1);
-      const bool inside = x1 < end_w1;                       // it ends inside the share of warp w1 ..
-      const bool own = inside && !(c0 == c1 && w0 == w1);    // .. with a slot of its own there
-      const int64_t first_w_last = c0 == c1 ? w0 : 0;        // first warp of the sequence in CTA c1
-      const bool joined_last = !inside || w1 > first_w_last; // CTA c1 also has a joined slot
-      // joined slots: (c0, w0), (c, 0) for the CTAs between, and c1's where there is one
-      s_range[0] = c0;
-      s_range[1] = joined_last ? c1 : c1 - 1;
-      s_range[2] = w0;
-      s_range[3] = own ? c1 * kDSlots + kDW + w1 : -1;
-      if (c0 == c1 && !own) s_range[1] = c0 - 1;  // written whole by its CTA or warp
+  const DecSeq sq = dec_seq(p, b);  // lens and starts do not change in this call
+  const int T = (sq.keys + 15) >> 4;
+  uint32_t q0, qn;
+  if (p.c.B <= kDMergeScan) {
+    __shared__ uint32_t s_sum[2];
+    if (threadIdx.x < 2) s_sum[threadIdx.x] = 0u;
+    __syncthreads();
+    const int i = static_cast<int>(threadIdx.x);
+    const uint32_t tiles = i < p.c.B ? static_cast<uint32_t>((dec_seq(p, i).keys + 15) >> 4) : 0u;
+    const uint32_t below = __reduce_add_sync(0xffffffffu, i < b ? tiles : 0u), all = __reduce_add_sync(0xffffffffu, tiles);
+    if ((i & 31) == 0) {
+      atomicAdd(&s_sum[0], below);
+      atomicAdd(&s_sum[1], all);
     }
+    __syncthreads();
+    q0 = s_sum[0];
+    qn = s_sum[1];
+    pdl_wait_primary();
+  } else {
+    pdl_wait_primary();
+    q0 = __ldcg(p.ws_pre + b);
+    qn = __ldcg(p.ws_pre + p.c.B);
   }
-  __syncthreads();
-  const int64_t c0 = s_range[0], c1 = s_range[1], w0 = s_range[2], own = s_range[3];
-  const int n = static_cast<int>(c1 - c0 + 1), total = n + (own >= 0 ? 1 : 0);
+  if (T == 0) return;
+  const int64_t X = static_cast<int64_t>(qn) * p.HG, x0 = static_cast<int64_t>(q0) * p.HG + static_cast<int64_t>(hg) * T;
+  const DecSlots sl = line_fits_int(X, grid)
+                          ? dec_slots<int, W>(static_cast<int>(x0), static_cast<int>(x0 + T), static_cast<int>(X), grid)
+                          : dec_slots<int64_t, W>(x0, x0 + T, X, grid);
+  const int total = sl.n + (sl.own >= 0 ? 1 : 0);
   if (total == 0) return;
-  auto slot = [&](int i) { return i == n ? own : (c0 + i) * kDSlots + (i == 0 ? w0 : 0); };
+  auto slot = [&](int i) { return static_cast<int64_t>(i == sl.n ? sl.own : (sl.c0 + i) * 2 * W + (i == 0 ? sl.w0 : 0)); };
   const int kvh = hg / p.NG, r0g = (hg - kvh * p.NG) * kHeads;
-  const DecSeq sq = dec_seq(p, b);
   const int nh = min(kHeads, sq.n * p.G - r0g);
   for (int i = threadIdx.x; i < nh * DH / 4; i += 256) {
     const int hd = i / (DH / 4);
-    float M = -INFINITY;
+    float M = -INFINITY, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     bool broken = false;
 #pragma unroll 4
     for (int k = 0; k < total; ++k) {
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot(k) * kHeads + hd);
-      M = fmaxf(M, ml.x);
-      broken |= ml.y < 0.f;
-    }
-    const float Mf = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < total; ++k) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot(k) * kHeads + hd);
       const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(k) * kHeads * DH) + i);
-      const float f = ex2(ml.x - Mf);
-      L = fmaf(f, ml.y, L);
-      O.x = fmaf(f, v.x, O.x);
-      O.y = fmaf(f, v.y, O.y);
-      O.z = fmaf(f, v.z, O.z);
-      O.w = fmaf(f, v.w, O.w);
+      broken |= ml.y < 0.f;
+      const float Mn = fmaxf(M, ml.x), ref = Mn == -INFINITY ? 0.f : Mn;
+      const float a = ex2(M - ref), f = ex2(ml.x - ref);
+      M = Mn;
+      L = fmaf(L, a, f * ml.y);
+      O.x = fmaf(O.x, a, f * v.x);
+      O.y = fmaf(O.y, a, f * v.y);
+      O.z = fmaf(O.z, a, f * v.z);
+      O.w = fmaf(O.w, a, f * v.w);
     }
     const float r = broken || L == 0.f ? 0.f : 1.f / L;
     const uint2 y = broken ? make_uint2(0u, 0u)
-                           : make_uint2(pack_bf16x2(O.x * r, O.y * r), pack_bf16x2(O.z * r, O.w * r));
+                           : make_uint2(round_bf16x2(O.x * r, O.y * r), round_bf16x2(O.z * r, O.w * r));
     const int rr = r0g + hd, j = rr / p.G;
     reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(sq.row0) + j) * p.Hq + static_cast<int64_t>(kvh) * p.G +
                                       (rr - j * p.G)) * DH)[i - hd * (DH / 4)] = y;
@@ -752,7 +826,7 @@ DecPlan dec_plan(const slim_paged_cache& c, int R) {
   d.NT = R <= 8 ? 1 : R <= 16 ? 2 : 4;
   d.NG = (R + 8 * d.NT - 1) / (8 * d.NT);
   d.HG = c.Hkv * d.NG;
-  const size_t slots = static_cast<size_t>(num_sms()) * kDSlots;
+  const size_t slots = static_cast<size_t>(num_sms()) * 2 * dec_warps(c.dtype == SLIM_E4M3, c.dh, d.NT);
   d.o_bytes = up256(slots * 8 * d.NT * c.dh * 4);
   d.ml_bytes = up256(slots * 8 * d.NT * 2 * 4);
   d.pre_bytes = up256((static_cast<size_t>(c.B) + 1) * 4);
@@ -762,12 +836,14 @@ DecPlan dec_plan(const slim_paged_cache& c, int R) {
 template <bool E, int DH, int NT>
 uint32_t dec_smem_bytes(int B, bool split) {
   using C = DecCfg<E, DH, NT>;
-  return static_cast<uint32_t>(kDW * kDRing + kDW * C::kStages * C::kTT * 2 * 4 + kDW * C::kHeads * 2 * 4 + kDW * 8 +
-                               kDW * 16 + (split ? (B + 1) * 4 : 0));
+  constexpr int W = C::kWarps;
+  return static_cast<uint32_t>(W * C::kRing + W * C::kStages * C::kTT * 2 * 4 + W * C::kHeads * 2 * 4 + W * sizeof(DecEnd) +
+                               (split ? (B + 1) * 4 : 0));
 }
 
 template <bool E, int DH, int NT>
 cudaError_t launch_dec(const PagedDecodeParams& p, cudaStream_t st, int* launches) {
+  using C = DecCfg<E, DH, NT>;
   const uint32_t smem = dec_smem_bytes<E, DH, NT>(p.c.B, p.split != 0);
   auto kern = paged_decode_kernel<E, DH, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -775,7 +851,7 @@ cudaError_t launch_dec(const PagedDecodeParams& p, cudaStream_t st, int* launche
   cudaLaunchConfig_t cfg = {};
   const int grid = p.split ? num_sms() : p.c.B * p.HG;
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kDThreads, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -793,7 +869,7 @@ cudaError_t launch_dec(const PagedDecodeParams& p, cudaStream_t st, int* launche
   cfg2.stream = st;
   cfg2.attrs = attr;
   cfg2.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg2, merge_paged_kernel<DH, NT>, p, static_cast<int64_t>(grid));
+  e = cudaLaunchKernelEx(&cfg2, merge_paged_kernel<DH, NT, C::kWarps>, p, grid);
   if (e == cudaSuccess && launches) ++*launches;
   return e;
 }

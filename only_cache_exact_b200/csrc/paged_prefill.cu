@@ -429,12 +429,13 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         if (valid < kFK && row >= valid) w = make_uint4(0u, 0u, 0u, 0u);
         uint8_t* box = dst + (cc >> 2) * 16384 + row * 128;
         const int c0 = (2 * cc) & 7, sw = row & 7;
-        *reinterpret_cast<uint4*>(box + ((c0 ^ sw) << 4)) =
-            make_uint4(e4m3x2_to_f16x2(w.x & 0xffffu), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y & 0xffffu),
-                       e4m3x2_to_f16x2(w.y >> 16));
-        *reinterpret_cast<uint4*>(box + (((c0 + 1) ^ sw) << 4)) =
-            make_uint4(e4m3x2_to_f16x2(w.z & 0xffffu), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w & 0xffffu),
-                       e4m3x2_to_f16x2(w.w >> 16));
+        uint32_t y[8];
+        e4m3x4_to_f16(w.x, y[0], y[1]);
+        e4m3x4_to_f16(w.y, y[2], y[3]);
+        e4m3x4_to_f16(w.z, y[4], y[5]);
+        e4m3x4_to_f16(w.w, y[6], y[7]);
+        *reinterpret_cast<uint4*>(box + ((c0 ^ sw) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(box + (((c0 + 1) ^ sw) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
       }
     };
     for (int i = 0; i < nkt; ++i) {
@@ -506,7 +507,9 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         for (int u = 0; u < 4; ++u) {
           const float y0 = bf16lo(x[u]) * inv, y1 = bf16hi(x[u]) * inv;
           hi[u] = to_e4m3x2(y0, y1);
-          const float2 g = e4m3x2_to_float2(hi[u]);
+          uint32_t back, none;
+          e4m3x4_to_f16(hi[u], back, none);
+          const float2 g = f16x2_to_float2(back);
           lo[u] = to_e4m3x2(y0 - g.x, y1 - g.y);
         }
         uint8_t* at = qs + t * T + rr * DH + (((c >> 1) ^ (DH == 128 ? rr & 7 : (rr >> 1) & 3)) << 4) + (c & 1) * 8;
@@ -585,13 +588,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           unpack2(ffma2(pack2(sc[32 * q + 2 * c], sc[32 * q + 2 * c + 1]), ff, pack2(e, e)), x0, x1);
           const float a = pf_ex2(x0), bb = pf_ex2(x1);
           s2[c >> 3] = fadd2(s2[c >> 3], pack2(a, bb));
-          if (E) {
-            const __half2 hv = __floats2half2_rn(a, bb);
-            pk[c] = *reinterpret_cast<const uint32_t*>(&hv);
-          } else {
-            const __nv_bfloat162 hv = __floats2bfloat162_rn(a, bb);
-            pk[c] = *reinterpret_cast<const uint32_t*>(&hv);
-          }
+          pk[c] = E ? round_f16x2(a, bb) : round_bf16x2(a, bb);
         }
         pf_tmem_st16(ts + lrow + static_cast<uint32_t>(16 * q), pk);
         sum0 = unpack_sum(s2[0]);
@@ -722,7 +719,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
             uint32_t y[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              y[k] = broken ? 0u : pack_bf16x2(v[16 * g + 2 * k] * inv, v[16 * g + 2 * k + 1] * inv);
+              y[k] = broken ? 0u : round_bf16x2(v[16 * g + 2 * k] * inv, v[16 * g + 2 * k + 1] * inv);
             w[2 * g] = make_uint4(y[0], y[1], y[2], y[3]);
             w[2 * g + 1] = make_uint4(y[4], y[5], y[6], y[7]);
           }
@@ -801,7 +798,7 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PagedPrefillPa
   const float inv = L == 0.f ? 0.f : 1.f / L;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * DH + lane * PL);
 #pragma unroll
-  for (int k = 0; k < PL; k += 2) dst[k / 2] = broken ? 0u : pack_bf16x2(o[k] * inv, o[k + 1] * inv);
+  for (int k = 0; k < PL; k += 2) dst[k / 2] = broken ? 0u : round_bf16x2(o[k] * inv, o[k + 1] * inv);
 }
 
 // Rows of a (sequence, key head) up to which the kernel of paged_decode.cu is taken: it streams the
