@@ -3,6 +3,8 @@
 // the scale rule.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -98,6 +100,19 @@ __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t round_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Host: raises a kernel's dynamic shared memory limit on the current device, once per device (the
+// call costs about as much as a launch's argument setup). `done` belongs to the kernel.
+inline cudaError_t allow_smem(const void* kern, uint32_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Host: the view of a checked cache.

@@ -846,7 +846,8 @@ cudaError_t launch_dec(const PagedDecodeParams& p, cudaStream_t st, int* launche
   using C = DecCfg<E, DH, NT>;
   const uint32_t smem = dec_smem_bytes<E, DH, NT>(p.c.B, p.split != 0);
   auto kern = paged_decode_kernel<E, DH, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), static_cast<uint32_t>(max_smem_optin()), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int grid = p.split ? num_sms() : p.c.B * p.HG;

@@ -833,7 +833,8 @@ cudaError_t launch_pf(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pa
                       int* launches) {
   using C = PfCfg<E, DHB>;
   auto kern = paged_prefill_kernel<E, DHB>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.c.Hkv) * p.pairs * p.splits, 1, 1);

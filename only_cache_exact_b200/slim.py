@@ -310,6 +310,7 @@ class PagedKV:
                 raise ValueError(f"{nm} is on another device")
         self.kpages, self.vpages, self.table, self.kscale, self.vscale = kpages, vpages, table, kscale, vscale
         self.dtype = dt
+        self._dev = kpages.get_device()
         self.num_pages, self.Hkv, self.page, self.dh = kpages.shape
         self.B, self.max_pages = table.shape
         self._c = _PagedCacheC(kpages.data_ptr(), vpages.data_ptr(), None if kscale is None else kscale.data_ptr(),
@@ -323,35 +324,40 @@ class PagedKV:
         return self.max_pages * self.page
 
 
-def _on_device(t, name: str, device, dtype, shape=None) -> int:
-    if t.device != device or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+# The paged calls take microseconds on the GPU, so what the binding does per tensor counts: device
+# numbers instead of device objects, and the stream's handle without a Stream object around it.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _on_device(t, name: str, dev: int, dtype, shape=None) -> int:
+    """Pointer of a contiguous tensor of this type (and shape) on CUDA device `dev`."""
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     return t.data_ptr()
 
 
-def _packed_rows(t, name: str, device, heads, dh: int):
-    """(pointer, row stride) of a bfloat16 [rows][heads][dh] tensor whose rows may lie apart."""
-    if t.device != device or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != dh or \
-            (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be bfloat16 [rows][{'heads' if heads is None else heads}][{dh}] on {device}")
+def _packed_rows(t, name: str, dev: int, heads, dh: int):
+    """(pointer, row stride, shape) of a bfloat16 [rows][heads][dh] tensor whose rows may lie apart."""
+    shape = t.shape
+    if t.get_device() != dev or t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != dh or \
+            (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be bfloat16 [rows][{'heads' if heads is None else heads}][{dh}] on cuda:{dev}")
     s0, s1, s2 = t.stride()
-    width = t.shape[1] * dh
-    if s2 != 1 or (s1 != dh and t.shape[1] > 1):
+    if s2 != 1 or (s1 != dh and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), (s0 if t.shape[0] > 1 else width)
+    return t.data_ptr(), (s0 if shape[0] > 1 else shape[1] * dh), shape
 
 
-def _paged_call(fn, where: str, device, stream, *args) -> None:
-    """Calls fn(*args, stream) with `device` current: a launch goes to the current device whatever its stream."""
-    if torch.cuda.current_device() == device.index:
-        s = torch.cuda.current_stream() if stream is None else stream
-        code = fn(*args, s.cuda_stream)
+def _paged_call(fn, where: str, dev: int, stream, *args) -> None:
+    """Calls fn(*args, stream) with `dev` current: a launch goes to the current device whatever its stream."""
+    if _current_device() == dev:
+        code = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            code = fn(*args, s.cuda_stream)
+        with torch.cuda.device(dev):
+            code = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if code != SLIM_OK:
         raise SlimError(code, where)
 
@@ -361,19 +367,20 @@ def slim_mha_paged_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, star
                           max_new: int = 0, stream=None) -> None:
     """Writes the packed rows k, v [rows][Hkv][dh] behind the lens[b] rows of every sequence; the keys (and
     q [rows][Hq][dh] into q_out) are rotated by cos, sin [n_pos][rot/2] float32. lens is not changed."""
-    dev, rows = cache.device, k.shape[0]
-    kp, ks = _packed_rows(k, "k", dev, cache.Hkv, cache.dh)
-    vp, vs = _packed_rows(v, "v", dev, cache.Hkv, cache.dh)
-    if v.shape[0] != rows or (q is None) != (q_out is None) or (cos is None) != (sin is None):
+    dev = cache._dev
+    kp, ks, shape = _packed_rows(k, "k", dev, cache.Hkv, cache.dh)
+    rows = shape[0]
+    vp, vs, vshape = _packed_rows(v, "v", dev, cache.Hkv, cache.dh)
+    if vshape[0] != rows or (q is None) != (q_out is None) or (cos is None) != (sin is None):
         raise ValueError("k and v need the same rows; q goes with q_out, cos with sin")
     qp = qo = None
     qs = Hq = 0
     if q is not None:
-        Hq = q.shape[1]
-        qp, qs = _packed_rows(q, "q", dev, Hq, cache.dh)
-        qo = _on_device(q_out, "q_out", dev, torch.bfloat16, (rows, Hq, cache.dh))
-        if q.shape[0] != rows:
+        qp, qs, shape = _packed_rows(q, "q", dev, None, cache.dh)
+        if shape[0] != rows:
             raise ValueError("q and k need the same rows")
+        Hq = shape[1]
+        qo = _on_device(q_out, "q_out", dev, torch.bfloat16, shape)
     cp = sp = None
     rot = n_pos = 0
     if cos is not None:
@@ -392,7 +399,7 @@ def slim_mha_paged_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, star
 def slim_mha_paged_gather(cache: PagedKV, first: torch.Tensor, starts: torch.Tensor, k_out: torch.Tensor,
                           v_out: torch.Tensor, status: torch.Tensor, max_new: int = 0, stream=None) -> None:
     """Rows first[b] .. of every sequence, starts[b+1]-starts[b] of them, packed as bfloat16 [rows][Hkv][dh]."""
-    dev, rows = cache.device, k_out.shape[0]
+    dev, rows = cache._dev, k_out.shape[0]
     shape = (rows, cache.Hkv, cache.dh)
     _paged_call(_lib.slim_mha_paged_gather, "slim_mha_paged_gather", dev, stream, cache._ref,
                 _on_device(starts, "starts", dev, torch.int32, (cache.B + 1,)),
@@ -420,13 +427,13 @@ def slim_mha_paged_decode(cache: PagedKV, q: torch.Tensor, lens: torch.Tensor, o
                           stream=None) -> None:
     """Attention of one query row per sequence, q [B][Hq][dh] bfloat16, over rows 0 .. lens[b]+rows_extra-1;
     out [B][Hq][dh] bfloat16."""
-    dev = cache.device
-    qp, qs = _packed_rows(q, "q", dev, None, cache.dh)
-    if q.shape[0] != cache.B:
+    dev = cache._dev
+    qp, qs, shape = _packed_rows(q, "q", dev, None, cache.dh)
+    if shape[0] != cache.B:
         raise ValueError("q must have one row per sequence")
     _paged_call(_lib.slim_mha_paged_decode, "slim_mha_paged_decode", dev, stream, cache._ref, qp, qs,
-                _on_device(lens, "lens", dev, torch.int32, (cache.B,)), rows_extra, q.shape[1], t_hint,
-                _on_device(out, "out", dev, torch.bfloat16, q.shape),
+                _on_device(lens, "lens", dev, torch.int32, (cache.B,)), rows_extra, shape[1], t_hint,
+                _on_device(out, "out", dev, torch.bfloat16, shape),
                 _on_device(workspace, "workspace", dev, torch.uint8), workspace.numel(),
                 _on_device(status, "status", dev, torch.int32))
 
@@ -449,12 +456,12 @@ def slim_mha_paged_prefill(cache: PagedKV, q: torch.Tensor, starts: torch.Tensor
                            t_hint: int = 0, stream=None) -> None:
     """Causal attention of the packed query rows q [rows][Hq][dh] bfloat16, row j of sequence b at position
     lens[b] + j, over the paged cache; out [rows][Hq][dh] bfloat16."""
-    dev, rows = cache.device, q.shape[0]
-    qp, qs = _packed_rows(q, "q", dev, None, cache.dh)
+    dev = cache._dev
+    qp, qs, shape = _packed_rows(q, "q", dev, None, cache.dh)
     _paged_call(_lib.slim_mha_paged_prefill, "slim_mha_paged_prefill", dev, stream, cache._ref, qp, qs,
                 _on_device(starts, "starts", dev, torch.int32, (cache.B + 1,)),
-                _on_device(lens, "lens", dev, torch.int32, (cache.B,)), rows, max_new, q.shape[1], t_hint,
-                _on_device(out, "out", dev, torch.bfloat16, q.shape),
+                _on_device(lens, "lens", dev, torch.int32, (cache.B,)), shape[0], max_new, shape[1], t_hint,
+                _on_device(out, "out", dev, torch.bfloat16, shape),
                 _on_device(workspace, "workspace", dev, torch.uint8), workspace.numel(),
                 _on_device(status, "status", dev, torch.int32))
 

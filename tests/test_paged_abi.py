@@ -116,17 +116,22 @@ def test_decode_refusals(S, kw, code):
     (dict(wsb=100), "EWORKSPACE"),
 ])
 def test_prefill_refusals(S, kw, code):
-    # 7 rows of 4 sequences over a capacity of 1280 rows: too few CTAs, so keys are split and need scratch
-    assert S.raw_lib().slim_mha_paged_prefill_workspace_bytes(cache(S), 32, 7, 0, 0) > 100
+    # both ways to run it need scratch: 7 rows of 4 heads take the few-row kernel, and 20 rows of 4 sequences over a
+    # capacity of 1280 rows have too few CTAs, so that keys are split
+    for rows in (7, 20):
+        assert S.raw_lib().slim_mha_paged_prefill_workspace_bytes(cache(S), 32, rows, 0, 0) > 100
     assert prefill(S, **kw) == getattr(S, "SLIM_" + code)
 
 
 def test_prefill_workspace(S):
     size = S.raw_lib().slim_mha_paged_prefill_workspace_bytes
-    assert size(cache(S), 32, 7, 0, 128) == 0       # short: one CTA walks all keys
+    assert size(cache(S), 32, 20, 0, 128) == 0      # short: one CTA walks all keys
     assert size(cache(S), 32, 8000, 0, 0) == 0      # many rows: CTAs enough
+    assert size(cache(S), 32, 20, 0, 0) > 0         # long cache, few CTAs
+    decode = S.raw_lib().slim_mha_paged_decode_workspace_bytes
+    assert size(cache(S), 8, 7, 1, 0) == decode(cache(S), 8)  # one row of a key head: the same kernel
     assert size(cache(S), 31, 7, 0, 0) == 0 and size(cache(S), 32, 0, 0, 0) == 0
-    assert size(cache(S), 32, 7, 0, 1 << 40) == size(cache(S), 32, 7, 0, 0)  # a hint past the capacity is the capacity
+    assert size(cache(S), 32, 20, 0, 1 << 40) == size(cache(S), 32, 20, 0, 0)  # a hint past the capacity is the capacity
 
 
 def test_nothing_to_do(S):
