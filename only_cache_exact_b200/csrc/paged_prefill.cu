@@ -42,7 +42,7 @@ constexpr int kFQ = 128;  // rows of a tile
 constexpr int kFK = 128;  // keys of a tile
 constexpr uint32_t kFTmemPerTile = 256;  // S (and P over it) at columns 0..127, O at 128
 constexpr float kFLazyLog2 = 8.f;
-constexpr int kFPart1 = 96;  // keys of P that are handed over first
+constexpr int kFSetup = 4;  // a CTA's fixed time in key tiles
 
 struct PagedPrefillParams {
   PagedView c;
@@ -63,6 +63,14 @@ struct PagedPrefillParams {
 
 template <bool E, int DHB>
 struct PfCfg {
+  // Keys of a step, the unit of S, softmax and P·V. Halves of a key tile (e4m3) have a TMEM region each, so
+  // that S of the next tile's half runs under the softmax of this one's other half: 816 -> 749 us for the
+  // 16K chunk. In bf16 the 64-key S MMAs cost as much shared-memory bandwidth as 128-key ones (their A
+  // operand is read either way) and the whole tile is faster: 544 -> 514 us for the 8192-token prompt.
+  static constexpr int FH = E ? 64 : 128;
+  static constexpr int HV = kFK / FH;                          // steps of a key tile
+  static constexpr int kPart1 = FH == 128 ? 96 : 64;           // keys of P that are handed over first
+  static constexpr int kParts = FH == 128 ? 2 : 1;
   static constexpr int DH = 64 * DHB;
   static constexpr int NK = E ? 3 : DHB == 2 ? 2 : 4;          // stages of the K ring
   static constexpr int NV = DHB == 2 ? 2 : 4;                  // stages of the V ring the MMAs read
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const PagedPrefillParams p) {
   using C = PfCfg<E, DHB>;
-  constexpr int DH = C::DH, NK = C::NK, NV = C::NV, NR = C::NR;
+  constexpr int DH = C::DH, NK = C::NK, NV = C::NV, NR = C::NR, FH = C::FH, HV = C::HV;
   constexpr uint32_t T = C::kTile, TK = C::kKTile;
   extern __shared__ uint8_t pf_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~uintptr_t(1023));
@@ -161,9 +169,10 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   uint64_t* kempty = kfull + NK;   // [NK]
   uint64_t* vfull = kempty + NK;   // [NV]
   uint64_t* vempty = vfull + NV;   // [NV]
-  uint64_t* sfull = vempty + NV;   // [2] S written
-  uint64_t* pready = sfull + 2;    // [part][2] P of the part's keys written over S (and O rescaled)
-  uint64_t* ofull = pready + 4;    // [2] the tile's last P·V MMA completed
+  uint64_t* sfull = vempty + NV;   // [row tile][half] S written
+  uint64_t* pready = sfull + 4;    // [row tile][half or part] P written over S (and O rescaled)
+  uint64_t* pvdone = pready + 4;   // [row tile] a P·V completed
+  uint64_t* ofull = pvdone + 2;    // [row tile] the tile's last P·V completed
   uint64_t* rfull = ofull + 2;     // [NR] raw V landed
   uint64_t* rempty = rfull + NR;   // [NR] raw V converted
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rempty + NR);
@@ -200,8 +209,13 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   const int nk_all = tile_keys(1);
   const int kt0 = static_cast<int>(static_cast<int64_t>(split) * nk_all / p.splits);
   const int kt1 = static_cast<int>(static_cast<int64_t>(split + 1) * nk_all / p.splits);
-  auto tile_end = [&](int t) { return max(kt0, min(kt1, tile_keys(t))); };
   const int nkt = kt1 - kt0;
+  // steps of this split that tile t attends
+  auto tile_steps = [&](int t) {
+    const int q0 = tile_q0(t);
+    const int all = q0 < 0 ? 0 : (len + min(q0 + p.QPT, n) - 1) / FH + 1;
+    return max(0, min(HV * kt1, all) - HV * kt0);
+  };
 
   if (warp == 0 && lane == 0) {
     mbar_init(qbar, 8);
@@ -217,10 +231,12 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       mbar_init(&rfull[s], 1);
       mbar_init(&rempty[s], 4);
     }
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 4; ++t) {
       mbar_init(&sfull[t], 1);
       mbar_init(&pready[t], 4);
-      mbar_init(&pready[2 + t], 4);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&pvdone[t], 1);
       mbar_init(&ofull[t], 1);
     }
     *s_bad = 0x7fffffff;
@@ -310,97 +326,103 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       // ------------------------------------------------------------ MMA issuer
       // The whole warp walks the loop and one elected lane issues, so that descriptors stay in uniform
       // registers: issued from a branch on the lane number, an MMA took 96 cycles instead of its 64.
-      const uint32_t idesc_s = E ? idesc_zero_f32(kFQ, kFK, 0u, 0u) : idesc_bf16_f32(kFQ, kFK, 0u, 0u);
+      const uint32_t idesc_s = E ? idesc_zero_f32(kFQ, FH, 0u, 0u) : idesc_bf16_f32(kFQ, FH, 0u, 0u);
       const uint32_t idesc_o = E ? idesc_zero_f32(kFQ, DH, 0u, 1u) : idesc_bf16_f32(kFQ, DH, 0u, 1u);
       // e4m3 rows of 64 bytes use the 64-byte swizzle, all others the 128-byte one
       constexpr uint32_t kLay = E && DH == 64 ? kLayoutSW64 : kLayoutSW128, kSbo = E && DH == 64 ? 512u : 1024u;
       const uint64_t qdesc = smem_desc(smem_u32(qs), 16, kSbo, kLay);
       const uint64_t kdesc = smem_desc(smem_u32(ks), 16, kSbo, kLay);
       const uint64_t vdesc = smem_desc(smem_u32(vs), 16384, 1024, kLayoutSW128);
-      const int nk0 = tile_end(0) - kt0, nk1 = nkt;
+      const int n0 = tile_steps(0), n1 = tile_steps(1);
       const bool lead = elect_one();
       bool ok = warp_wait(qbar, 0u, p.status);
-      // S_t(i) = Q_t·K_i^T; the caller has waited for K_i
-      auto issue_s = [&](int t, int s) {
+      // S_t(u) = Q_t·K^T of half hf of the key tile in stage s; the caller has waited for it
+      auto issue_s = [&](int t, int hf, int s, bool release) {
         tc_fence_after();
         if (lead) {
-          const uint64_t kd = kdesc + static_cast<uint32_t>(s) * (TK >> 4), qd = qdesc + static_cast<uint32_t>(t) * (T >> 4);
+          const uint32_t d = tmem + t * kFTmemPerTile + hf * FH;
+          const uint64_t qd = qdesc + static_cast<uint32_t>(t) * (T >> 4);
+          const uint64_t kd = kdesc + static_cast<uint32_t>(s) * (TK >> 4) + static_cast<uint32_t>(hf) * (E ? FH * DH >> 4 : FH * 8);
           if (E) {
 #pragma unroll
             for (int kk = 0; kk < DH / 32; ++kk)  // high and low part of Q on the same K columns
 #pragma unroll
               for (int part = 0; part < 2; ++part)
-                pf_umma_f8(tmem + t * kFTmemPerTile, qd + part * (T >> 5) + kk * 2u, kd + kk * 2u, idesc_s,
-                           kk + part > 0 ? 1u : 0u);
+                pf_umma_f8(d, qd + part * (T >> 5) + kk * 2u, kd + kk * 2u, idesc_s, kk + part > 0 ? 1u : 0u);
           } else {
 #pragma unroll
             for (int kk = 0; kk < DH / 16; ++kk) {
               const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
-              umma_f16(tmem + t * kFTmemPerTile, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+              umma_f16(d, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
             }
           }
-          umma_commit(&sfull[t]);
-          if (t == 1) umma_commit(&kempty[s]);
+          umma_commit(&sfull[2 * t + hf]);
+          if (release) umma_commit(&kempty[s]);
         }
       };
-      // O_t += P_t(i)·V_i, in two parts: the first kFPart1 keys start while the softmax works on the rest
-      auto issue_pv = [&](int t, int i, int s) {
-        const uint32_t par = static_cast<uint32_t>(i) & 1u, pt = tmem + t * kFTmemPerTile;
-        const uint64_t vd = vdesc + static_cast<uint32_t>(s) * (T >> 4);
-        if (!warp_wait(&pready[t], par, p.status)) return false;
-        tc_fence_after();
-        if (lead) {
+      // O_t += P_t(u)·V of the step's keys; of a whole tile the first part starts while the softmax works
+      // on the rest
+      auto issue_pv = [&](int t, int u, int s, bool release) {
+        const int hf = HV == 2 ? u & 1 : 0;
+        const uint32_t par = static_cast<uint32_t>(u / HV) & 1u;
+        const uint32_t o = tmem + t * kFTmemPerTile + 128u, pt = tmem + t * kFTmemPerTile + hf * FH;
+        const uint64_t vd = vdesc + static_cast<uint32_t>(s) * (T >> 4) + static_cast<uint32_t>(hf) * (FH / 16 * 128);
 #pragma unroll
-          for (int kk = 0; kk < kFPart1 / 16; ++kk)
-            pf_umma_tmem_a(pt + 128u, pt + static_cast<uint32_t>(kk * 8), vd + static_cast<uint32_t>(kk * 128), idesc_o,
-                           (i > 0 || kk > 0) ? 1u : 0u);
+        for (int part = 0; part < C::kParts; ++part) {
+          if (!warp_wait(&pready[2 * t + (HV == 2 ? hf : part)], par, p.status)) return false;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int kk = part ? C::kPart1 / 16 : 0; kk < (part + 1 == C::kParts ? FH : C::kPart1) / 16; ++kk)
+              pf_umma_tmem_a(o, pt + static_cast<uint32_t>(kk * 8), vd + static_cast<uint32_t>(kk * 128), idesc_o,
+                             (u > 0 || kk > 0) ? 1u : 0u);
+          }
         }
-        if (!warp_wait(&pready[2 + t], par, p.status)) return false;
-        tc_fence_after();
         if (lead) {
-#pragma unroll
-          for (int kk = kFPart1 / 16; kk < kFK / 16; ++kk)
-            pf_umma_tmem_a(pt + 128u, pt + static_cast<uint32_t>(kk * 8), vd + static_cast<uint32_t>(kk * 128), idesc_o,
-                           1u);
-          if (t == 1) umma_commit(&vempty[s]);
+          if (HV == 2) umma_commit(&pvdone[t]);
+          if (release) umma_commit(&vempty[s]);
         }
         return true;
       };
       bool committed0 = false, committed1 = false;
-      if (ok && nk1 > 0) {
+      if (ok && n1 > 0) {
         ok = warp_wait(&kfull[0], 0u, p.status);
-        if (ok && nk0 > 0) issue_s(0, 0);
-        if (ok) issue_s(1, 0);
+        for (int hf = 0; ok && hf < HV; ++hf) {
+          if (hf < n0) issue_s(0, hf, 0, false);
+          if (hf < n1) issue_s(1, hf, 0, hf == HV - 1 || n1 == 1);
+        }
       }
-      int sv = 0, sk = 1;  // V stage of i, K stage of i + 1
+      int sv = 0, sk = 1;  // V stage of the key tile, K stage of the next one
       uint32_t phv = 0u, phk = 0u;
-      for (int i = 0; ok && i < nk1; ++i) {
-        const bool more = i + 1 < nk1;
-        ok = warp_wait(&vfull[sv], phv, p.status) && (!more || warp_wait(&kfull[sk], phk, p.status));
-        if (!ok) break;
-        if (i < nk0) {
-          if (!(ok = issue_pv(0, i, sv))) break;
-          if (i == nk0 - 1) {
+      for (int u = 0; ok && u < n1; ++u) {
+        const int hf = HV == 2 ? u & 1 : 0;
+        if (hf == 0) {
+          ok = warp_wait(&vfull[sv], phv, p.status) && (u + HV >= n1 || warp_wait(&kfull[sk], phk, p.status));
+          if (!ok) break;
+        }
+        if (u < n0) {
+          if (!(ok = issue_pv(0, u, sv, false))) break;
+          if (u == n0 - 1) {
             if (lead) umma_commit(&ofull[0]);
             committed0 = true;
-          } else {
-            issue_s(0, sk);  // overwrites the P that the P·V above reads: issued after it
           }
+          if (u + HV < n0) issue_s(0, hf, sk, false);  // overwrites the P that the P·V above reads: issued after it
         }
-        if (!(ok = issue_pv(1, i, sv))) break;
-        if (!more) {
+        if (!(ok = issue_pv(1, u, sv, hf == HV - 1 || u == n1 - 1))) break;
+        if (u == n1 - 1) {
           if (lead) umma_commit(&ofull[1]);
           committed1 = true;
-        } else {
-          issue_s(1, sk);
         }
-        if (++sv == NV) {
-          sv = 0;
-          phv ^= 1u;
-        }
-        if (++sk == NK) {
-          sk = 0;
-          phk ^= 1u;
+        if (u + HV < n1) issue_s(1, hf, sk, hf == HV - 1 || u + HV + 1 == n1);
+        if (hf == HV - 1) {
+          if (++sv == NV) {
+            sv = 0;
+            phv ^= 1u;
+          }
+          if (++sk == NK) {
+            sk = 0;
+            phk ^= 1u;
+          }
         }
       }
       // also after a failure: each output barrier covers every MMA issued
@@ -413,29 +435,27 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     // ------------------------------------------------------------ codes to f16
     reg_dec<64>();
     const int tid = threadIdx.x - 384;
-    constexpr int CPR = DH / 16;  // 16-code chunks of a row
-    // A warp takes 32 / CPR rows at a time. At dh = 128 eight lanes read four chunks of one row and the
-    // other four of the next, and write two rows of different swizzle parity: every phase of the read
-    // and of both writes meets eight different 16-byte banks.
+    constexpr int CPR = DH / 16;        // 16-code chunks of a row
+    constexpr int RS = 128 / CPR;       // rows that the four warps take at a time
+    // At dh = 128 eight lanes read four chunks of one row and the other four of the next, and write two
+    // rows of different swizzle parity: every phase of the read and of both writes meets eight different
+    // 16-byte banks. RS is a multiple of 8, so that the swizzle stays the same from turn to turn.
+    const int row0 = CPR == 8 ? (tid >> 4) * 2 + ((tid >> 2) & 1) : tid / CPR;
+    const int cc = CPR == 8 ? (tid & 3) + 4 * (((tid >> 2) ^ (tid >> 3)) & 1) : tid % CPR;
+    const int src0 = row0 * DH + cc * 16, box0 = (cc >> 2) * 16384 + row0 * 128;
+    const int dst0 = box0 + ((((2 * cc) & 7) ^ (row0 & 7)) << 4), dst1 = box0 + ((((2 * cc + 1) & 7) ^ (row0 & 7)) << 4);
     auto convert = [&](const uint8_t* raw, uint8_t* dst, int valid) {
-#pragma unroll 4
-      for (int u = tid; u < kFK * CPR; u += 128) {
-        int row = u / CPR, cc = u - row * CPR;
-        if (CPR == 8) {
-          row = (u >> 4) * 2 + ((u >> 2) & 1);
-          cc = (u & 3) + 4 * (((u >> 2) ^ (u >> 3)) & 1);
-        }
-        uint4 w = *reinterpret_cast<const uint4*>(raw + row * DH + cc * 16);
-        if (valid < kFK && row >= valid) w = make_uint4(0u, 0u, 0u, 0u);
-        uint8_t* box = dst + (cc >> 2) * 16384 + row * 128;
-        const int c0 = (2 * cc) & 7, sw = row & 7;
+#pragma unroll
+      for (int k = 0; k < kFK / RS; ++k) {
+        uint4 w = *reinterpret_cast<const uint4*>(raw + src0 + k * RS * DH);
+        if (valid < kFK && row0 + k * RS >= valid) w = make_uint4(0u, 0u, 0u, 0u);
         uint32_t y[8];
         e4m3x4_to_f16(w.x, y[0], y[1]);
         e4m3x4_to_f16(w.y, y[2], y[3]);
         e4m3x4_to_f16(w.z, y[4], y[5]);
         e4m3x4_to_f16(w.w, y[6], y[7]);
-        *reinterpret_cast<uint4*>(box + ((c0 ^ sw) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint4*>(box + (((c0 + 1) ^ sw) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+        *reinterpret_cast<uint4*>(dst + dst0 + k * RS * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(dst + dst1 + k * RS * 128) = make_uint4(y[4], y[5], y[6], y[7]);
       }
     };
     for (int i = 0; i < nkt; ++i) {
@@ -443,7 +463,11 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       if (!warp_wait(&rfull[sr], static_cast<uint32_t>(i / NR) & 1u, p.status) ||
           (i >= NV && !warp_wait(&vempty[s], static_cast<uint32_t>(i / NV - 1) & 1u, p.status)))
         break;
-      convert(rv + sr * C::kRaw, vs + s * T, Lz - (kt0 + i) * kFK);
+      const int valid = Lz - (kt0 + i) * kFK;
+      if (valid >= kFK)
+        convert(rv + sr * C::kRaw, vs + s * T, kFK);
+      else
+        convert(rv + sr * C::kRaw, vs + s * T, valid);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -459,8 +483,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     const int row = quarter * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lrow = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + t * kFTmemPerTile, tmem_o = ts + 128u;
-    const int q0 = tile_q0(t), nkt_t = tile_end(t) - kt0;
-    const int nkt_below = t > 0 ? tile_end(0) - kt0 : 0;  // key tiles that the lower tile attends too
+    const int q0 = tile_q0(t), steps = tile_steps(t), nkt_t = (steps + HV - 1) / HV;
+    const int nkt_below = t > 0 ? (tile_steps(0) + HV - 1) / HV : 0;  // key tiles that the lower tile attends too
     auto div_g = [&](int x) { return static_cast<int>((static_cast<uint32_t>(x) * p.g_inv) >> 16); };
     const int qi = q0 + div_g(row), head = h * p.G + row - div_g(row) * p.G;
     const bool live = q0 >= 0 && row < p.QPT * p.G && qi < n;
@@ -480,76 +504,115 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           wv[k / RI] = __ldg(reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(r.row0) + rq) * p.q_stride +
                                                             (static_cast<int64_t>(h) * p.G + rr - qd * p.G) * DH) + c);
       }
+      if (!E) {
 #pragma unroll
-      for (int k = 0; k < 32; k += RI) {
-        const int rr = quarter * 32 + k + lane / LR;
-        const uint4 w = wv[k / RI];
-        if (!E) {
-          *reinterpret_cast<uint4*>(qs + t * T + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = w;
-          continue;
+        for (int k = 0; k < 32; k += RI) {
+          const int rr = quarter * 32 + k + lane / LR;
+          *reinterpret_cast<uint4*>(qs + t * T + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = wv[k / RI];
         }
-        // in units that bring the row's largest magnitude to [128, 256): a high and a low e4m3 part hold
-        // the 8 bits of a bf16 exactly down to 2^-10 of it, and 2^-17 of it is the error below
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-        uint32_t amax = 0u;
+      } else {
+        // In units that bring the row's largest magnitude to [128, 256): a high and a low e4m3 part hold
+        // the 8 bits of a bf16 exactly down to 2^-10 of it, and 2^-17 of it is the error below. The
+        // maxima of all rows first, so that their shuffles overlap.
+        uint32_t amax[32 / RI];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) amax = max(amax, max(x[u] & 0x7fffu, (x[u] >> 16) & 0x7fffu));
-#pragma unroll
-        for (int o = 1; o < LR; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const int e = max(-118, min(126, static_cast<int>(amax >> 7) - 127));
-        const float inv = exp2_int(7 - e);
-        float f = exp2_int(e) * 0.0078125f * p.scale_log2;
-        if (amax >= 0x7f80u) f = __uint_as_float(0x7fc00000u);  // e4m3 has no infinity
-        f = __shfl_sync(0xffffffffu, f, (lane % RI) * LR);
-        if (lane / RI == k / RI) fq = f;
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float y0 = bf16lo(x[u]) * inv, y1 = bf16hi(x[u]) * inv;
-          hi[u] = to_e4m3x2(y0, y1);
-          uint32_t back, none;
-          e4m3x4_to_f16(hi[u], back, none);
-          const float2 g = f16x2_to_float2(back);
-          lo[u] = to_e4m3x2(y0 - g.x, y1 - g.y);
+        for (int k = 0; k < 32 / RI; ++k) {
+          const uint32_t x[4] = {wv[k].x & 0x7fff7fffu, wv[k].y & 0x7fff7fffu, wv[k].z & 0x7fff7fffu, wv[k].w & 0x7fff7fffu};
+          const uint32_t y = __vmaxu2(__vmaxu2(x[0], x[1]), __vmaxu2(x[2], x[3]));
+          amax[k] = max(y & 0xffffu, y >> 16);
         }
-        uint8_t* at = qs + t * T + rr * DH + (((c >> 1) ^ (DH == 128 ? rr & 7 : (rr >> 1) & 3)) << 4) + (c & 1) * 8;
-        *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-        *reinterpret_cast<uint2*>(at + T / 2) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+#pragma unroll
+        for (int o = 1; o < LR; o <<= 1)
+#pragma unroll
+          for (int k = 0; k < 32 / RI; ++k) amax[k] = max(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
+#pragma unroll
+        for (int k = 0; k < 32; k += RI) {
+          const int rr = quarter * 32 + k + lane / LR;
+          const uint32_t x[4] = {wv[k / RI].x, wv[k / RI].y, wv[k / RI].z, wv[k / RI].w}, am = amax[k / RI];
+          const int e = max(-118, min(126, static_cast<int>(am >> 7) - 127));
+          const float inv = exp2_int(7 - e);
+          float f = exp2_int(e) * 0.0078125f * p.scale_log2;
+          if (am >= 0x7f80u) f = __uint_as_float(0x7fc00000u);  // e4m3 has no infinity
+          f = __shfl_sync(0xffffffffu, f, (lane % RI) * LR);
+          if (lane / RI == k / RI) fq = f;
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float y0 = bf16lo(x[u]) * inv, y1 = bf16hi(x[u]) * inv;
+            hi[u] = to_e4m3x2(y0, y1);
+            uint32_t back, none;
+            e4m3x4_to_f16(hi[u], back, none);
+            const float2 g = f16x2_to_float2(back);
+            lo[u] = to_e4m3x2(y0 - g.x, y1 - g.y);
+          }
+          uint8_t* at = qs + t * T + rr * DH + (((c >> 1) ^ (DH == 128 ? rr & 7 : (rr >> 1) & 3)) << 4) + (c & 1) * 8;
+          *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(at + T / 2) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qbar);
     }
     // e4m3: scales of a key tile's pages, one page per lane, fetched a tile ahead
-    auto fetch = [&](int i, float& ksc, float& vsc) {  // key scale and the value scale's exponent
+    // (and their page numbers two ahead: the scales' addresses wait for them)
+    auto page_ahead = [&](int i) {
+      const int j = kt0 + i;
+      return i < nkt_t && lane < pages_of(j) ? page_id(j * ppt + lane) : -1;
+    };
+    auto fetch = [&](int id, float& ksc, float& vsc) {  // key scale and the value scale's exponent
       ksc = 1.f;
       vsc = 0.f;
-      const int j = kt0 + i;
-      if (i < nkt_t && lane < pages_of(j)) {
-        const int64_t at = static_cast<int64_t>(page_id(j * ppt + lane)) * p.c.Hkv + h;
+      if (id >= 0) {
+        const int64_t at = static_cast<int64_t>(id) * p.c.Hkv + h;
         ksc = __ldg(p.c.ks + at);
-        vsc = scale_log2(__ldg(p.c.vs + at));
+        vsc = __ldg(p.c.vs + at);
       }
     };
-    float ks_next = 1.f, lv_next = 0.f;
-    if (E) fetch(0, ks_next, lv_next);
+    float ks_next = 1.f, vs_next = 0.f, ks_lane = 1.f, lv_lane = 0.f;
+    int id_next = -1;
+    if (E) {
+      fetch(page_ahead(0), ks_next, vs_next);
+      id_next = page_ahead(1);
+    }
     float m = -INFINITY, l = 0.f;
+    float ksu = 1.f, lvu = 0.f;
+    bool uniform = true;  // one scale pair for all pages of the key tile
     bool ok = true;
-    for (int i = 0; i < nkt_t; ++i) {
-      const int s = i % NV;
-      const float ks_lane = ks_next, lv_lane = lv_next;
-      if (E) fetch(i + 1, ks_next, lv_next);
-      if (!__all_sync(0xffffffffu, mbar_wait(&sfull[t], static_cast<uint32_t>(i) & 1u, p.status))) {
+#pragma unroll 1
+    for (int u = 0; u < steps; ++u) {
+      const int i = u / HV, hf = HV == 2 ? u & 1 : 0;
+      const uint32_t ph = static_cast<uint32_t>(i) & 1u, tsh = ts + lrow + static_cast<uint32_t>(hf * FH);
+      if (E && hf == 0) {
+        ks_lane = ks_next;
+        lv_lane = scale_log2(vs_next);
+        fetch(id_next, ks_next, vs_next);
+        id_next = page_ahead(i + 2);
+      }
+      const int kt = (kt0 + i) * kFK, k0 = kt + hf * FH;
+      // bf16: key rows from Lz on are zeroed in V (thread r takes key row r, once the tile's V has
+      // landed) by the lowest tile that attends this key tile, before it hands over its first P
+      if (!E && hf == 0 && kt + kFK > Lz && i >= nkt_below) {
+        const int s = i % NV;
+        if (kt + row >= Lz && mbar_wait(&vfull[s], static_cast<uint32_t>(i / NV) & 1u, p.status)) {
+          uint8_t* vrow = vs + s * T + row * 128;
+#pragma unroll
+          for (int k = 0; k < DHB; ++k)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + k * 16384 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      if (!warp_wait(&sfull[2 * t + hf], ph, p.status)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      float sc[kFK];
+      float sc[FH];
 #pragma unroll
-      for (int c = 0; c < kFK / 16; ++c)
-        tmem_ld16(ts + lrow + static_cast<uint32_t>(16 * c), *reinterpret_cast<float(*)[16]>(sc + 16 * c));
+      for (int c = 0; c < FH / 16; ++c)
+        tmem_ld16(tsh + static_cast<uint32_t>(16 * c), *reinterpret_cast<float(*)[16]>(sc + 16 * c));
       tmem_wait_ld();
-      const int k0 = (kt0 + i) * kFK;
       // Running maximum of the weights' exponents: of the scores in log2 units, for e4m3 plus the value
       // scale's exponent lv, so that P stays in f16's range whatever the pages' scales are. P of key t
       // is 2^(s_t + e), e = lv - m, and l adds P·2^-lv. Where a group's largest P is below 2^-60 (its
@@ -563,9 +626,11 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           m = mt;
           l *= alpha;
         }
-        // O is rescaled before P is handed over. The tensor cores are done with it: S of this key tile
-        // was issued after the last P·V, and its barrier covers that too.
-        if (i >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // O is rescaled before P is handed over, once the step before's P·V is done with it (a whole
+        // tile's S was issued after it)
+        if (u >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (HV == 2) ok = warp_wait(&pvdone[t], static_cast<uint32_t>(u - 1) & 1u, p.status);
+          tc_fence_after();
           for (int c = 0; c < DH; c += 16) {
             float v[16];
             tmem_ld16(tmem_o + lrow + static_cast<uint32_t>(c), v);
@@ -576,7 +641,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           }
         }
       };
-      // P of keys 32 q .. 32 q + 31 to tensor memory; the sums of either half
+      // P of keys 32 q .. 32 q + 31 of the step to tensor memory; the sums of either half of them
       auto weights = [&](int q, float f, float e0, float e1, float& sum0, float& sum1) {
         uint32_t pk[16];
         uint64_t s2[2] = {0ull, 0ull};
@@ -590,50 +655,36 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           s2[c >> 3] = fadd2(s2[c >> 3], pack2(a, bb));
           pk[c] = E ? round_f16x2(a, bb) : round_bf16x2(a, bb);
         }
-        pf_tmem_st16(ts + lrow + static_cast<uint32_t>(16 * q), pk);
+        pf_tmem_st16(tsh + static_cast<uint32_t>(16 * q), pk);
         sum0 = unpack_sum(s2[0]);
         sum1 = unpack_sum(s2[1]);
       };
-      // hands a part of P (and, before the first, the zeroed V rows and O) to the MMA warp
-      auto hand_over = [&](int part) {
+      // hands P (and, before its first part, the zeroed V rows and O) to the MMA warp
+      auto hand_over = [&](int k) {
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[2 * part + t]);
+        if (lane == 0) mbar_arrive(&pready[2 * t + k]);
       };
-      // bf16: key rows from Lz on are zeroed in V (thread r takes key row r, once the tile's V has
-      // landed) by the lowest tile that attends this key tile
-      if (!E && k0 + kFK > Lz && i >= nkt_below) {
-        if (k0 + row >= Lz && mbar_wait(&vfull[s], static_cast<uint32_t>(i / NV) & 1u, p.status)) {
-          uint8_t* vrow = vs + s * T + row * 128;
-#pragma unroll
-          for (int k = 0; k < DHB; ++k)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + k * 16384 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-      }
-      float ksu = 1.f, lvu = 0.f;
-      bool uniform = true;  // one scale pair for all pages of the tile
-      if (E) {
+      if (E && hf == 0) {
         ksu = __shfl_sync(0xffffffffu, ks_lane, 0);
         lvu = __shfl_sync(0xffffffffu, lv_lane, 0);
         uniform = __all_sync(0xffffffffu, lane >= pages_of(kt0 + i) || (ks_lane == ksu && lv_lane == lvu));
       }
       if (uniform) {
         const float f = E ? fq * ksu : p.scale_log2;
-        if (k0 + kFK - 1 > pos) {
+        if (k0 + FH - 1 > pos) {
 #pragma unroll
-          for (int c = 0; c < kFK; ++c) sc[c] = (k0 + c <= pos) ? sc[c] : -INFINITY;
+          for (int c = 0; c < FH; ++c) sc[c] = (k0 + c <= pos) ? sc[c] : -INFINITY;
         }
         float mx[4] = {sc[0], sc[1], sc[2], sc[3]};
 #pragma unroll
-        for (int c = 4; c + 8 <= kFK; c += 8) {
+        for (int c = 4; c + 8 <= FH; c += 8) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], sc[c + k], sc[c + 4 + k]);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], sc[kFK - 4 + k]);
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], sc[FH - 4 + k]);
         const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
         advance(mt + lvu);
         const float mm = m == -INFINITY ? 0.f : m;
@@ -641,20 +692,20 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         if (E && mt != -INFINITY && e < -60.f - mt) e = -60.f - mt;
         float total = 0.f;
 #pragma unroll
-        for (int q = 0; q < kFK / 32; ++q) {
+        for (int q = 0; q < FH / 32; ++q) {
           float s0, s1;
           weights(q, f, e, e, s0, s1);
           total += s0 + s1;
-          if (32 * (q + 1) == kFPart1) hand_over(0);
+          if (C::kParts == 2 && 32 * (q + 1) == C::kPart1) hand_over(0);
         }
-        hand_over(1);
         l += E ? total * pf_ex2(-mm - e) : total;
       } else {
-        float lv[kFK / 16], mg[kFK / 16], top = -INFINITY;
+        float lv[FH / 16], mg[FH / 16], top = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < kFK / 16; ++g) {
-          const float f = __shfl_sync(0xffffffffu, ks_lane, (g * 16) >> psh) * fq;
-          lv[g] = __shfl_sync(0xffffffffu, lv_lane, (g * 16) >> psh);
+        for (int g = 0; g < FH / 16; ++g) {
+          const int pg = (hf * FH + g * 16) >> psh;
+          const float f = __shfl_sync(0xffffffffu, ks_lane, pg) * fq;
+          lv[g] = __shfl_sync(0xffffffffu, lv_lane, pg);
           mg[g] = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -666,7 +717,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         advance(top);
         const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int q = 0; q < kFK / 32; ++q) {
+        for (int q = 0; q < FH / 32; ++q) {
           float e[2], s2[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -676,14 +727,16 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           }
           weights(q, 1.f, e[0], e[1], s2[0], s2[1]);
           l += s2[0] * pf_ex2(-mm - e[0]) + s2[1] * pf_ex2(-mm - e[1]);
-          if (32 * (q + 1) == kFPart1) hand_over(0);
+          if (C::kParts == 2 && 32 * (q + 1) == C::kPart1) hand_over(0);
         }
-        hand_over(1);
       }
+      if (!ok) break;
+      hand_over(HV == 2 ? hf : C::kParts - 1);
     }
+    tmem_wait_st();
     // ------------------------------------------------------------ o = O / l, or the split's partial
     bool got = ok;
-    if (nkt_t > 0) got = ok && __all_sync(0xffffffffu, mbar_wait(&ofull[t], 0u, p.status));
+    if (steps > 0) got = ok && __all_sync(0xffffffffu, mbar_wait(&ofull[t], 0u, p.status));
     tc_fence_after();
     const bool broken = pos >= *s_bad;
     // 128 bytes of every row at a time go through the warp's part of the Q tile (no MMA reads it any
@@ -730,10 +783,10 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       const int64_t first = static_cast<int64_t>(split) * p.rows * p.Hq;
       if (live) {
         const int64_t prow = first + (static_cast<int64_t>(r.row0) + qi) * p.Hq + head;
-        p.ws_ml[prow * 2] = nkt_t > 0 && got ? m : -INFINITY;
-        p.ws_ml[prow * 2 + 1] = broken ? -1.f : nkt_t > 0 && got ? l : 0.f;
+        p.ws_ml[prow * 2] = steps > 0 && got ? m : -INFINITY;
+        p.ws_ml[prow * 2 + 1] = broken ? -1.f : steps > 0 && got ? l : 0.f;
       }
-      if (nkt_t > 0) {
+      if (steps > 0) {
 #pragma unroll 1
         for (int c = 0; c < DH; c += 32) {
           uint4 w[8];
@@ -818,10 +871,23 @@ PfPlan pf_plan(const slim_paged_cache& c, int Hq, int64_t rows, int64_t max_new,
   const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page;
   const int64_t hint = t_hint > 0 ? std::min(t_hint, cap) : cap;
   f.pairs = static_cast<int>((max_new + 2 * f.QPT - 1) / (2 * f.QPT));
-  // as many ranges of keys as there are SMs for, of four key tiles at least
-  const int64_t ctas = static_cast<int64_t>(c.B) * c.Hkv * f.pairs;
-  const int64_t by_sms = num_sms() / std::max<int64_t>(ctas, 1), by_keys = hint / (4 * kFK);
-  f.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(by_sms, by_keys), 64)));
+  // Ranges of keys: as many as make the waves of CTAs end together soonest. A CTA's time is its key tiles
+  // and about kFSetup tiles more (query, first S, output); how many pairs of row tiles there are follows
+  // from the rows up to half a pair per sequence.
+  const int sms = num_sms();
+  const int64_t nk = (hint + kFK - 1) / kFK;
+  const int64_t some = std::min<int64_t>(static_cast<int64_t>(c.B) * f.pairs, rows / (2 * f.QPT) + (c.B + 1) / 2);
+  const int64_t ctas = std::max<int64_t>(1, some) * c.Hkv;
+  double best = 0;
+  f.splits = 1;
+  for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, nk / 4)); ++s) {
+    const double waves = static_cast<double>((ctas * s + sms - 1) / sms);
+    const double cost = waves * (static_cast<double>(nk) / s + kFSetup + (s > 1 ? 2 : 0));
+    if (s == 1 || cost < 0.95 * best) {
+      best = cost;
+      f.splits = static_cast<int>(s);
+    }
+  }
   const size_t items = f.splits > 1 ? static_cast<size_t>(f.splits) * rows * Hq : 0;
   f.o_bytes = pf_up256(items * c.dh * 4);
   f.ml_bytes = pf_up256(items * 8);
