@@ -11,9 +11,9 @@
 // It walks the 128-key tiles up to its last query's position.
 //   warp 0        loads K and V, page by page, by TMA straight into the MMAs' swizzled layouts;
 //                 e4m3 values as bulk copies of whole page heads into a raw ring
-//   warp 1        issues tcgen05.mma: S_t = Q_t·K^T into the tile's TMEM S region,
-//                 O_t += P_t·V with P_t read from tensor memory, in the order
-//                 P_0(j)·V_j, S_0(j+1), P_1(j)·V_j, S_1(j+1)
+//   warps 1, 2    issue tcgen05.mma for one row tile each: S_t = Q_t·K^T into the tile's
+//                 TMEM S region, O_t += P_t·V with P_t read from tensor memory, in the
+//                 order P_t(j)·V_j, S_t(j+1)
 //   warps 4..7, 8..11  softmax of tile 0 and 1, one row per thread: causal mask,
 //                 lazy running maximum (O is rescaled only when a maximum grows by
 //                 more than 2^8), P over the S region, row sums in fp32
@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   uint64_t* pready = sfull + 4;    // [row tile][half or part] P written over S (and O rescaled)
   uint64_t* pvdone = pready + 4;   // [row tile] a P·V completed
   uint64_t* ofull = pvdone + 2;    // [row tile] the tile's last P·V completed
-  uint64_t* rfull = ofull + 2;     // [NR] raw V landed
+  uint64_t* vfixed = ofull + 2;    // [NV] bf16: V rows past the end are zeroed
+  uint64_t* rfull = vfixed + NV;     // [NR] raw V landed
   uint64_t* rempty = rfull + NR;   // [NR] raw V converted
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rempty + NR);
   int* s_bad = reinterpret_cast<int*>(tmem_slot + 1);  // first position whose page is outside the pool
@@ -221,11 +222,12 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     mbar_init(qbar, 8);
     for (int s = 0; s < NK; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+      mbar_init(&kempty[s], 2);
     }
     for (int s = 0; s < NV; ++s) {
       mbar_init(&vfull[s], E ? 4 : 1);
-      mbar_init(&vempty[s], 1);
+      mbar_init(&vempty[s], 2);
+      mbar_init(&vfixed[s], 1);
     }
     for (int s = 0; s < NR; ++s) {
       mbar_init(&rfull[s], 1);
@@ -322,50 +324,61 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         mbar_wait(&kfull[u % NK], static_cast<uint32_t>(u / NK) & 1u, p.status);
       for (int u = max(0, nv_issued - N); u < nv_issued; ++u)
         mbar_wait(E ? &rfull[u % N] : &vfull[u % N], static_cast<uint32_t>(u / N) & 1u, p.status);
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      // The whole warp walks the loop and one elected lane issues, so that descriptors stay in uniform
-      // registers: issued from a branch on the lane number, an MMA took 96 cycles instead of its 64.
+    } else if (warp <= 2) {
+      // ------------------------------------------------------------ MMA issuer of row tile t
+      // One warp per row tile: a wait takes about 120 cycles and a commit 100 where an MMA takes 64, and
+      // one warp for both tiles spent its whole time on them. The whole warp walks the loop and one elected
+      // lane issues, so that descriptors stay in uniform registers: issued from a branch on the lane
+      // number, an MMA took 96 cycles.
+      const int t = warp - 1;
       const uint32_t idesc_s = E ? idesc_zero_f32(kFQ, FH, 0u, 0u) : idesc_bf16_f32(kFQ, FH, 0u, 0u);
       const uint32_t idesc_o = E ? idesc_zero_f32(kFQ, DH, 0u, 1u) : idesc_bf16_f32(kFQ, DH, 0u, 1u);
       // e4m3 rows of 64 bytes use the 64-byte swizzle, all others the 128-byte one
       constexpr uint32_t kLay = E && DH == 64 ? kLayoutSW64 : kLayoutSW128, kSbo = E && DH == 64 ? 512u : 1024u;
-      const uint64_t qdesc = smem_desc(smem_u32(qs), 16, kSbo, kLay);
+      const uint64_t qdesc = smem_desc(smem_u32(qs) + t * T, 16, kSbo, kLay);
       const uint64_t kdesc = smem_desc(smem_u32(ks), 16, kSbo, kLay);
       const uint64_t vdesc = smem_desc(smem_u32(vs), 16384, 1024, kLayoutSW128);
-      const int n0 = tile_steps(0), n1 = tile_steps(1);
+      const uint32_t tmem_t = tmem + t * kFTmemPerTile;
+      const int steps = tile_steps(t);
+      // key tiles that only this row tile reads: it releases them for both
+      const int alone = t == 1 ? (tile_steps(0) + HV - 1) / HV : 0x7fffffff;
+      const int first_fix = E ? 0x7fffffff : max(0, Lz / kFK - kt0);  // first key tile with rows past Lz
       const bool lead = elect_one();
       bool ok = warp_wait(qbar, 0u, p.status);
-      // S_t(u) = Q_t·K^T of half hf of the key tile in stage s; the caller has waited for it
-      auto issue_s = [&](int t, int hf, int s, bool release) {
+      auto release = [&](uint64_t* bar, int i) {
+        umma_commit(bar);
+        if (i >= alone) umma_commit(bar);
+      };
+      // S(u) = Q·K^T of the step's keys, stage s; the caller has waited for it
+      auto issue_s = [&](int u, int s) {
+        const int hf = HV == 2 ? u & 1 : 0;
         tc_fence_after();
         if (lead) {
-          const uint32_t d = tmem + t * kFTmemPerTile + hf * FH;
-          const uint64_t qd = qdesc + static_cast<uint32_t>(t) * (T >> 4);
+          const uint32_t d = tmem_t + hf * FH;
           const uint64_t kd = kdesc + static_cast<uint32_t>(s) * (TK >> 4) + static_cast<uint32_t>(hf) * (E ? FH * DH >> 4 : FH * 8);
           if (E) {
 #pragma unroll
             for (int kk = 0; kk < DH / 32; ++kk)  // high and low part of Q on the same K columns
 #pragma unroll
               for (int part = 0; part < 2; ++part)
-                pf_umma_f8(d, qd + part * (T >> 5) + kk * 2u, kd + kk * 2u, idesc_s, kk + part > 0 ? 1u : 0u);
+                pf_umma_f8(d, qdesc + part * (T >> 5) + kk * 2u, kd + kk * 2u, idesc_s, kk + part > 0 ? 1u : 0u);
           } else {
 #pragma unroll
             for (int kk = 0; kk < DH / 16; ++kk) {
               const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
-              umma_f16(d, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+              umma_f16(d, qdesc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
             }
           }
           umma_commit(&sfull[2 * t + hf]);
-          if (release) umma_commit(&kempty[s]);
+          if (hf == HV - 1 || u == steps - 1) release(&kempty[s], u / HV);
         }
       };
-      // O_t += P_t(u)·V of the step's keys; of a whole tile the first part starts while the softmax works
-      // on the rest
-      auto issue_pv = [&](int t, int u, int s, bool release) {
+      // O += P(u)·V of the step's keys; of a whole tile the first part starts while the softmax works on
+      // the rest
+      auto issue_pv = [&](int u, int s) {
         const int hf = HV == 2 ? u & 1 : 0;
         const uint32_t par = static_cast<uint32_t>(u / HV) & 1u;
-        const uint32_t o = tmem + t * kFTmemPerTile + 128u, pt = tmem + t * kFTmemPerTile + hf * FH;
+        const uint32_t o = tmem_t + 128u, pt = tmem_t + hf * FH;
         const uint64_t vd = vdesc + static_cast<uint32_t>(s) * (T >> 4) + static_cast<uint32_t>(hf) * (FH / 16 * 128);
 #pragma unroll
         for (int part = 0; part < C::kParts; ++part) {
@@ -380,40 +393,39 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         }
         if (lead) {
           if (HV == 2) umma_commit(&pvdone[t]);
-          if (release) umma_commit(&vempty[s]);
+          if (hf == HV - 1 || u == steps - 1) release(&vempty[s], u / HV);
         }
         return true;
       };
-      bool committed0 = false, committed1 = false;
-      if (ok && n1 > 0) {
+      if (ok && steps > 0) {
         ok = warp_wait(&kfull[0], 0u, p.status);
-        for (int hf = 0; ok && hf < HV; ++hf) {
-          if (hf < n0) issue_s(0, hf, 0, false);
-          if (hf < n1) issue_s(1, hf, 0, hf == HV - 1 || n1 == 1);
-        }
+        for (int u = 0; ok && u < min(HV, steps); ++u) issue_s(u, 0);
       }
       int sv = 0, sk = 1;  // V stage of the key tile, K stage of the next one
       uint32_t phv = 0u, phk = 0u;
-      for (int u = 0; ok && u < n1; ++u) {
-        const int hf = HV == 2 ? u & 1 : 0;
+      for (int u = 0; ok && u < steps; ++u) {
+        const int hf = HV == 2 ? u & 1 : 0, i = u / HV;
         if (hf == 0) {
-          ok = warp_wait(&vfull[sv], phv, p.status) && (u + HV >= n1 || warp_wait(&kfull[sk], phk, p.status));
+          ok = warp_wait(&vfull[sv], phv, p.status) && (u + HV >= steps || warp_wait(&kfull[sk], phk, p.status));
           if (!ok) break;
-        }
-        if (u < n0) {
-          if (!(ok = issue_pv(0, u, sv, false))) break;
-          if (u == n0 - 1) {
-            if (lead) umma_commit(&ofull[0]);
-            committed0 = true;
+          // bf16: key rows from Lz on are zeroed in V by tile 1's warp (it attends every key tile of the CTA)
+          // before either tile's first P·V that reads them
+          if (i >= first_fix) {
+            if (t == 1) {
+              for (int k = max(0, Lz - (kt0 + i) * kFK) * 8 + lane; k < kFK * 8; k += 32)
+#pragma unroll
+                for (int box = 0; box < DHB; ++box)
+                  *reinterpret_cast<uint4*>(vs + sv * T + box * 16384 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&vfixed[sv]);
+            } else if (!(ok = warp_wait(&vfixed[sv], static_cast<uint32_t>((i - first_fix) / NV) & 1u, p.status))) {
+              break;
+            }
           }
-          if (u + HV < n0) issue_s(0, hf, sk, false);  // overwrites the P that the P·V above reads: issued after it
         }
-        if (!(ok = issue_pv(1, u, sv, hf == HV - 1 || u == n1 - 1))) break;
-        if (u == n1 - 1) {
-          if (lead) umma_commit(&ofull[1]);
-          committed1 = true;
-        }
-        if (u + HV < n1) issue_s(1, hf, sk, hf == HV - 1 || u + HV + 1 == n1);
+        if (!(ok = issue_pv(u, sv))) break;
+        if (u + HV < steps) issue_s(u + HV, sk);  // overwrites the P that the P·V above reads: issued after it
         if (hf == HV - 1) {
           if (++sv == NV) {
             sv = 0;
@@ -425,11 +437,9 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           }
         }
       }
-      // also after a failure: each output barrier covers every MMA issued
-      if (lead && !committed0) umma_commit(&ofull[0]);
-      if (lead && !committed1) umma_commit(&ofull[1]);
-      warp_wait(&ofull[0], 0u, p.status);
-      warp_wait(&ofull[1], 0u, p.status);
+      // also after a failure: the output barrier covers every MMA issued
+      if (lead) umma_commit(&ofull[t]);
+      warp_wait(&ofull[t], 0u, p.status);
     }
   } else if (E && warp >= 12) {
     // ------------------------------------------------------------ codes to f16
@@ -484,7 +494,6 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     const uint32_t lrow = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + t * kFTmemPerTile, tmem_o = ts + 128u;
     const int q0 = tile_q0(t), steps = tile_steps(t), nkt_t = (steps + HV - 1) / HV;
-    const int nkt_below = t > 0 ? (tile_steps(0) + HV - 1) / HV : 0;  // key tiles that the lower tile attends too
     auto div_g = [&](int x) { return static_cast<int>((static_cast<uint32_t>(x) * p.g_inv) >> 16); };
     const int qi = q0 + div_g(row), head = h * p.G + row - div_g(row) * p.G;
     const bool live = q0 >= 0 && row < p.QPT * p.G && qi < n;
@@ -589,20 +598,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         fetch(id_next, ks_next, vs_next);
         id_next = page_ahead(i + 2);
       }
-      const int kt = (kt0 + i) * kFK, k0 = kt + hf * FH;
-      // bf16: key rows from Lz on are zeroed in V (thread r takes key row r, once the tile's V has
-      // landed) by the lowest tile that attends this key tile, before it hands over its first P
-      if (!E && hf == 0 && kt + kFK > Lz && i >= nkt_below) {
-        const int s = i % NV;
-        if (kt + row >= Lz && mbar_wait(&vfull[s], static_cast<uint32_t>(i / NV) & 1u, p.status)) {
-          uint8_t* vrow = vs + s * T + row * 128;
-#pragma unroll
-          for (int k = 0; k < DHB; ++k)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + k * 16384 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-      }
+      const int k0 = (kt0 + i) * kFK + hf * FH;
       if (!warp_wait(&sfull[2 * t + hf], ph, p.status)) {
         ok = false;
         break;
@@ -659,7 +655,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         sum0 = unpack_sum(s2[0]);
         sum1 = unpack_sum(s2[1]);
       };
-      // hands P (and, before its first part, the zeroed V rows and O) to the MMA warp
+      // hands P (and, before its first part, O) to the MMA warp
       auto hand_over = [&](int k) {
         tmem_wait_st();
         tc_fence_before();
