@@ -79,7 +79,7 @@ struct PfCfg {
   static constexpr uint32_t kKTile = E ? kFK * DH : kTile;     // bytes of a K tile
   static constexpr uint32_t kRaw = E ? kFK * DH : 0u;          // bytes of a raw V tile
   static constexpr int kThreads = E ? 512 : 384;
-  static constexpr uint32_t kSmem = 2u * kTile + NK * kKTile + NV * kTile + NR * kRaw + 512u + 1024u;
+  static constexpr uint32_t kSmem = 2u * kTile + NK * kKTile + NV * kTile + NR * kRaw + 512u + 1024u + 1024u;
 };
 
 __device__ __forceinline__ float pf_ex2(float x) {
@@ -178,6 +178,9 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   uint64_t* rempty = rfull + NR;   // [NR] raw V converted
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rempty + NR);
   int* s_bad = reinterpret_cast<int*>(tmem_slot + 1);  // first position whose page is outside the pool
+  // e4m3: [key tile mod 8] scale of its pages if they share one (key scale, value exponent, whether), then
+  // key scale and value exponent of each page. Written by the K producer before the tile's barrier.
+  float* s_scale = reinterpret_cast<float*>(bars + 64);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   pdl_launch_dependents();
@@ -279,15 +282,37 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     if (warp == 0) {
       // ------------------------------------------------------------ loads
       int nk_issued = 0, nv_issued = 0;
-      int id_next = nkt > 0 && lane < pages_of(kt0) ? page_id(kt0 * ppt + lane) : 0;
+      // page numbers two key tiles ahead and, for e4m3, their scales one ahead
+      auto page_ahead = [&](int i) { return i < nkt && lane < pages_of(kt0 + i) ? page_id((kt0 + i) * ppt + lane) : -1; };
+      auto scale_of = [&](const float* pool, int id) {
+        return E && id >= 0 ? __ldg(pool + static_cast<int64_t>(id) * p.c.Hkv + h) : 1.f;
+      };
+      int id = page_ahead(0), id_next = page_ahead(1);
+      float ks_l = scale_of(p.c.ks, id), vs_l = scale_of(p.c.vs, id);
       for (int i = 0; i < nkt; ++i) {
-        const int j = kt0 + i, npg = pages_of(j), id = id_next;
-        if (i + 1 < nkt) id_next = lane < pages_of(j + 1) ? page_id((j + 1) * ppt + lane) : 0;
+        const int npg = pages_of(kt0 + i);
         const uint32_t bytes = static_cast<uint32_t>(npg << psh) * DH * (E ? 1u : 2u);
         const int y = (id * p.c.Hkv + h) << psh;  // first line of the page's head
         const uint32_t line = static_cast<uint32_t>(lane << psh);
         const int sk = i % NK;
         if (i >= NK && !warp_wait(&kempty[sk], static_cast<uint32_t>(i / NK - 1) & 1u, p.status)) break;
+        if (E) {
+          const float lv_l = scale_log2(vs_l), ks0 = __shfl_sync(0xffffffffu, ks_l, 0), lv0 = __shfl_sync(0xffffffffu, lv_l, 0);
+          const bool one = __all_sync(0xffffffffu, lane >= npg || (ks_l == ks0 && lv_l == lv0));
+          float* sc = s_scale + (i & 7) * 20;
+          if (lane < 8) {
+            sc[4 + 2 * lane] = ks_l;
+            sc[5 + 2 * lane] = lv_l;
+          }
+          if (lane == 0) {
+            sc[0] = ks0;
+            sc[1] = lv0;
+            sc[2] = one ? 1.f : 0.f;
+          }
+          ks_l = scale_of(p.c.ks, id_next);
+          vs_l = scale_of(p.c.vs, id_next);
+          __syncwarp();
+        }
         if (lane == 0) mbar_arrive_expect_tx(&kfull[sk], bytes);
         __syncwarp();
         if (lane < npg) {
@@ -317,6 +342,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           }
         }
         ++nv_issued;
+        id = id_next;
+        id_next = page_ahead(i + 2);
       }
       // every issued copy lands before the CTA exits
       constexpr int N = E ? NR : NV;
@@ -493,7 +520,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     const int row = quarter * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lrow = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + t * kFTmemPerTile, tmem_o = ts + 128u;
-    const int q0 = tile_q0(t), steps = tile_steps(t), nkt_t = (steps + HV - 1) / HV;
+    const int q0 = tile_q0(t), steps = tile_steps(t);
     auto div_g = [&](int x) { return static_cast<int>((static_cast<uint32_t>(x) * p.g_inv) >> 16); };
     const int qi = q0 + div_g(row), head = h * p.G + row - div_g(row) * p.G;
     const bool live = q0 >= 0 && row < p.QPT * p.G && qi < n;
@@ -563,27 +590,6 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(qbar);
     }
-    // e4m3: scales of a key tile's pages, one page per lane, fetched a tile ahead
-    // (and their page numbers two ahead: the scales' addresses wait for them)
-    auto page_ahead = [&](int i) {
-      const int j = kt0 + i;
-      return i < nkt_t && lane < pages_of(j) ? page_id(j * ppt + lane) : -1;
-    };
-    auto fetch = [&](int id, float& ksc, float& vsc) {  // key scale and the value scale's exponent
-      ksc = 1.f;
-      vsc = 0.f;
-      if (id >= 0) {
-        const int64_t at = static_cast<int64_t>(id) * p.c.Hkv + h;
-        ksc = __ldg(p.c.ks + at);
-        vsc = __ldg(p.c.vs + at);
-      }
-    };
-    float ks_next = 1.f, vs_next = 0.f, ks_lane = 1.f, lv_lane = 0.f;
-    int id_next = -1;
-    if (E) {
-      fetch(page_ahead(0), ks_next, vs_next);
-      id_next = page_ahead(1);
-    }
     float m = -INFINITY, l = 0.f;
     float ksu = 1.f, lvu = 0.f;
     bool uniform = true;  // one scale pair for all pages of the key tile
@@ -592,12 +598,6 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     for (int u = 0; u < steps; ++u) {
       const int i = u / HV, hf = HV == 2 ? u & 1 : 0;
       const uint32_t ph = static_cast<uint32_t>(i) & 1u, tsh = ts + lrow + static_cast<uint32_t>(hf * FH);
-      if (E && hf == 0) {
-        ks_lane = ks_next;
-        lv_lane = scale_log2(vs_next);
-        fetch(id_next, ks_next, vs_next);
-        id_next = page_ahead(i + 2);
-      }
       const int k0 = (kt0 + i) * kFK + hf * FH;
       if (!warp_wait(&sfull[2 * t + hf], ph, p.status)) {
         ok = false;
@@ -662,10 +662,12 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[2 * t + k]);
       };
+      const float* sc_scale = s_scale + (i & 7) * 20;
       if (E && hf == 0) {
-        ksu = __shfl_sync(0xffffffffu, ks_lane, 0);
-        lvu = __shfl_sync(0xffffffffu, lv_lane, 0);
-        uniform = __all_sync(0xffffffffu, lane >= pages_of(kt0 + i) || (ks_lane == ksu && lv_lane == lvu));
+        const float4 w = *reinterpret_cast<const float4*>(sc_scale);
+        ksu = w.x;
+        lvu = w.y;
+        uniform = w.z != 0.f;
       }
       if (uniform) {
         const float f = E ? fq * ksu : p.scale_log2;
@@ -700,8 +702,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
 #pragma unroll
         for (int g = 0; g < FH / 16; ++g) {
           const int pg = (hf * FH + g * 16) >> psh;
-          const float f = __shfl_sync(0xffffffffu, ks_lane, pg) * fq;
-          lv[g] = __shfl_sync(0xffffffffu, lv_lane, pg);
+          const float f = sc_scale[4 + 2 * pg] * fq;
+          lv[g] = sc_scale[5 + 2 * pg];
           mg[g] = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
