@@ -299,8 +299,8 @@ int slim_mha_decode_step(const float* q, const void* k_new, const void* v_new, v
  * max_new) and SLIM_DEV_OVERFLOW (lens[b] plus the new rows above cap) skip the
  * sequence: nothing of it is written to the cache, and its output rows are
  * zero (where its starts are valid). SLIM_DEV_BADPAGE: rows of that page are not written, and
- * outputs that would read it are zero. Keys and values of attended rows must
- * be finite; whatever lies in the pages behind a sequence's rows is never used.
+ * outputs that would read it are zero. Queries, and keys and values of attended rows,
+ * must be finite; whatever lies in the pages behind a sequence's rows is never used.
  *
  * Return codes of all calls: SLIM_EINVAL for a null or misaligned pointer
  * (16 bytes), a size out of range or head counts that do not divide;

@@ -19,6 +19,14 @@ constexpr int kScaleExpMin = -100;
 constexpr int kScaleExpMax = 120;
 constexpr int kPagedMaxB = 4096;  // the decode plan holds one line offset per sequence in shared memory
 
+// Plain loads for everything an earlier kernel of the stream may have written (lengths, page tables,
+// scales, queries): these kernels are launched while that one may still run and wait for it inside, so
+// nothing is constant for their whole lifetime as the read-only path requires.
+template <typename T>
+__device__ __forceinline__ T ld_plain(const T* p) {
+  return *p;
+}
+
 struct PagedView {
   uint8_t* k;
   uint8_t* v;
@@ -34,7 +42,7 @@ struct PagedView {
 
   // page number of row t, or -1 where it is outside the pool
   __device__ __forceinline__ int page_of(int b, int64_t t) const {
-    const int id = __ldg(table + static_cast<int64_t>(b) * max_pages + (t >> page_shift));
+    const int id = ld_plain(table + static_cast<int64_t>(b) * max_pages + (t >> page_shift));
     return id >= 0 && id < num_pages ? id : -1;
   }
 };
@@ -51,13 +59,12 @@ struct PagedRows {
 __device__ __forceinline__ PagedRows paged_rows(const int32_t* starts, const int32_t* lens, int b, int64_t rows,
                                                 int64_t max_new, int64_t cap, int64_t limit) {
   PagedRows r;
-  const int s0 = __ldg(starts + b), s1 = __ldg(starts + b + 1);
-  r.len = __ldg(lens + b);
+  const int s0 = ld_plain(starts + b), s1 = ld_plain(starts + b + 1);
+  r.len = ld_plain(lens + b);
   r.row0 = s0;
-  r.n = s1 - s0;
   r.bits = 0;
   r.span = s0 >= 0 && s1 >= s0 && s1 <= rows;
-  if (!r.span) r.n = 0;
+  r.n = r.span ? s1 - s0 : 0;
   if (!r.span || r.n > max_new || r.len < 0 || r.len > cap)
     r.bits = SLIM_DEV_BADLEN;
   else if (static_cast<int64_t>(r.len) + r.n > (cap < limit ? cap : limit) && r.n > 0)

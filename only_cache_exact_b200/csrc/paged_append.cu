@@ -86,7 +86,7 @@ __device__ __forceinline__ void rotate_unit(const RawUnit& raw, bool turn, const
   float c[8], s[8];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float4 cv = __ldg(reinterpret_cast<const float4*>(cs) + i), sv = __ldg(reinterpret_cast<const float4*>(sn) + i);
+    const float4 cv = ld_plain(reinterpret_cast<const float4*>(cs) + i), sv = ld_plain(reinterpret_cast<const float4*>(sn) + i);
     c[4 * i] = cv.x, c[4 * i + 1] = cv.y, c[4 * i + 2] = cv.z, c[4 * i + 3] = cv.w;
     s[4 * i] = sv.x, s[4 * i + 1] = sv.y, s[4 * i + 2] = sv.z, s[4 * i + 3] = sv.w;
   }
@@ -398,9 +398,9 @@ __global__ void __launch_bounds__(kAppThreads) gather_kernel(const GatherParams 
     for (int h = h0; h < h1; ++h) {
       uint4 o0 = make_uint4(0u, 0u, 0u, 0u), o1 = o0;
       if (id >= 0) {
-        o0 = __ldg(reinterpret_cast<const uint4*>(at + h * p.c.head_bytes));
+        o0 = ld_plain(reinterpret_cast<const uint4*>(at + h * p.c.head_bytes));
         if (kE4M3) {
-          const float s = __ldg(scales + h);
+          const float s = ld_plain(scales + h);
           uint32_t y[8];
           e4m3x4_to_f16(o0.x, y[0], y[1]);
           e4m3x4_to_f16(o0.y, y[2], y[3]);
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kAppThreads) gather_kernel(const GatherParams 
           o0 = make_uint4(y[0], y[1], y[2], y[3]);
           o1 = make_uint4(y[4], y[5], y[6], y[7]);
         } else {
-          o1 = __ldg(reinterpret_cast<const uint4*>(at + h * p.c.head_bytes) + 1);
+          o1 = ld_plain(reinterpret_cast<const uint4*>(at + h * p.c.head_bytes) + 1);
         }
       }
       to[h * (DH / 8)] = o0;

@@ -117,7 +117,7 @@ __device__ __forceinline__ DecSeq dec_seq(const PagedDecodeParams& p, int b) {
     s.keys = r.bits || r.n == 0 ? 0 : r.len + r.n;
     return s;
   }
-  const int L = __ldg(p.lens + b);
+  const int L = ld_plain(p.lens + b);
   s.row0 = b;
   s.n = 1;
   s.span = true;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
   auto window = [&]() {  // page numbers of tiles l_tile .. l_tile + 31
     l_win = l_tile;
     const int t = l_tile + lane;
-    l_id = t < ls.end ? __ldg(p.c.table + static_cast<int64_t>(ls.b) * p.c.max_pages +
+    l_id = t < ls.end ? ld_plain(p.c.table + static_cast<int64_t>(ls.b) * p.c.max_pages +
                               ((static_cast<int64_t>(t) * 16) >> p.c.page_shift))
                       : 0;
   };
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
         uint32_t amax = 0u;
 #pragma unroll
         for (int j = 0; j < DH / 16; ++j) {
-          w[j] = hd < nh ? __ldg(reinterpret_cast<const uint2*>(src + 16 * j + 4 * lq)) : make_uint2(0u, 0u);
+          w[j] = hd < nh ? ld_plain(reinterpret_cast<const uint2*>(src + 16 * j + 4 * lq)) : make_uint2(0u, 0u);
           amax = max(max(amax, w[j].x & 0x7fffu), max((w[j].x >> 16) & 0x7fffu, w[j].y & 0x7fffu));
           amax = max(amax, (w[j].y >> 16) & 0x7fffu);
         }
@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
       } else {
 #pragma unroll
         for (int j = 0; j < DH / 16; ++j) {
-          qf[n][j][0] = hd < nh ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * j + 2 * lq)) : 0u;
-          qf[n][j][1] = hd < nh ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * j + 8 + 2 * lq)) : 0u;
+          qf[n][j][0] = hd < nh ? ld_plain(reinterpret_cast<const uint32_t*>(src + 16 * j + 2 * lq)) : 0u;
+          qf[n][j][1] = hd < nh ? ld_plain(reinterpret_cast<const uint32_t*>(src + 16 * j + 8 + 2 * lq)) : 0u;
         }
         hs[n][0] = hs[n][1] = p.scale_log2;
       }

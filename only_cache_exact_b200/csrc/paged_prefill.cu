@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   const int page_lo = kt0 * ppt, page_hi = min(kt1 * ppt, ((L - 1) >> psh) + 1);
   int first_bad = 0x7fffffff;
   for (int i = page_lo + static_cast<int>(threadIdx.x); i < page_hi; i += C::kThreads) {
-    const int id = __ldg(table + i);
+    const int id = ld_plain(table + i);
     if (id < 0 || id >= p.c.num_pages) first_bad = min(first_bad, i << psh);
   }
   tc_fence_before();
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
 
   // page number of page i of the sequence for the loads: page 0 where it is outside the pool
   auto page_id = [&](int i) {
-    const int id = __ldg(table + i);
+    const int id = ld_plain(table + i);
     return id >= 0 && id < p.c.num_pages ? id : 0;
   };
   // pages of key tile j that hold rows of the sequence
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       // page numbers two key tiles ahead and, for e4m3, their scales one ahead
       auto page_ahead = [&](int i) { return i < nkt && lane < pages_of(kt0 + i) ? page_id((kt0 + i) * ppt + lane) : -1; };
       auto scale_of = [&](const float* pool, int id) {
-        return E && id >= 0 ? __ldg(pool + static_cast<int64_t>(id) * p.c.Hkv + h) : 1.f;
+        return E && id >= 0 ? ld_plain(pool + static_cast<int64_t>(id) * p.c.Hkv + h) : 1.f;
       };
       int id = page_ahead(0), id_next = page_ahead(1);
       float ks_l = scale_of(p.c.ks, id), vs_l = scale_of(p.c.vs, id);
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         const int rr = quarter * 32 + k + lane / LR, qd = div_g(rr), rq = q0 + qd;
         wv[k / RI] = make_uint4(0u, 0u, 0u, 0u);
         if (q0 >= 0 && rr < p.QPT * p.G && rq < n)
-          wv[k / RI] = __ldg(reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(r.row0) + rq) * p.q_stride +
+          wv[k / RI] = ld_plain(reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(r.row0) + rq) * p.q_stride +
                                                             (static_cast<int64_t>(h) * p.G + rr - qd * p.G) * DH) + c);
       }
       if (!E) {
