@@ -670,7 +670,9 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         uniform = w.z != 0.f;
       }
       if (uniform) {
-        const float f = E ? fq * ksu : p.scale_log2;
+        // below fp32's range the scores are zero either way, but the mask's -inf must not meet a zero factor
+        float f = E ? fq * ksu : p.scale_log2;
+        if (E && f < 1.2e-38f) f = 1.2e-38f;  // a NaN scale stays
         if (k0 + FH - 1 > pos) {
 #pragma unroll
           for (int c = 0; c < FH; ++c) sc[c] = (k0 + c <= pos) ? sc[c] : -INFINITY;

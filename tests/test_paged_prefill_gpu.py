@@ -229,6 +229,24 @@ def test_large_scores_and_scales(S, kind, t_hint):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [5, 200])
+@pytest.mark.parametrize("t_hint", [1, 0])
+def test_zero_queries_small_keys(S, kind, new, t_hint):
+    """Padding rows of zeros beside ordinary ones, over keys so small that the factor of a zero row's scores leaves
+    fp32's range: equal weights, also where the causal mask ends inside a tile."""
+    st = PagedState(S, kind, 1, 64, 16, [600], [600], seed=30)
+    for w in (st.scales if kind == "e4m3" else st.pages)[:1]:
+        w *= 2.0 ** -60
+    st.oracle[0].values = st.oracle[0].values * 2.0 ** -60
+    n, cached = [new], [600 - new]
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows(n, 3)
+    q[: new // 2] = 0
+    out = run(S, st, q, n, cached, max_new=new, t_hint=t_hint)
+    check(st, q, out, n, cached)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_chunks_then_tokens(S, kind):
     """A prompt in chunks, each appended and attended, then single tokens: a model layer's use of the cache, captured
     per chunk size and on a stream of its own."""
