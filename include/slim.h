@@ -281,7 +281,8 @@ int slim_mha_decode_step(const float* q, const void* k_new, const void* v_new, v
  *   table           int32[B][max_pages]; entries past a sequence's rows are
  *                   not read. Several sequences may read one page; a page that
  *                   slim_mha_paged_append writes to must occur once.
- *   num_pages, max_pages >= 1; num_pages*Hkv*page and max_pages*page < 2^31
+ *   num_pages, max_pages >= 1; num_pages*Hkv*page < 2^31, max_pages*page <= 2^30,
+ *                   B*max_pages*page <= 2^35
  *   dtype           SLIM_BF16 or SLIM_E4M3
  *   B               1..4096 sequences;   Hkv 1..1024 key/value heads
  *   dh              64 or 128;   page 16, 32, 64 or 128 rows
@@ -293,14 +294,17 @@ int slim_mha_decode_step(const float* q, const void* k_new, const void* v_new, v
  * of [rows][heads][dh] arrays. Rows outside [starts[0], starts[B]) are neither
  * read nor written.
  *
- * max_new is the caller's bound on starts[b+1]-starts[b] (0: `rows`); it sizes
- * the launch. Device status, OR-ed into *dev_status: SLIM_DEV_BADLEN (lens[b]
- * outside [0, cap], starts not ascending within [0, rows], more rows than
- * max_new) and SLIM_DEV_OVERFLOW (lens[b] plus the new rows above cap) skip the
- * sequence: nothing of it is written to the cache, and its output rows are
- * zero (where its starts are valid). SLIM_DEV_BADPAGE: rows of that page are not written, and
- * outputs that would read it are zero. Queries, and keys and values of attended rows,
- * must be finite; whatever lies in the pages behind a sequence's rows is never used.
+ * max_new is the caller's bound on starts[b+1]-starts[b] (0: `rows`). It sizes
+ * the launch for every sequence, so that a bound well above the longest one
+ * costs CTAs that find nothing to do, and it picks the kernel: 1 for steps of
+ * single tokens. Device status, OR-ed into *dev_status: SLIM_DEV_BADLEN
+ * (lens[b] outside [0, cap], starts not ascending within [0, rows], more rows
+ * than max_new) and SLIM_DEV_OVERFLOW (lens[b] plus the new rows above cap)
+ * skip the sequence: nothing of it is written to the cache, and its output
+ * rows are zero (where its starts are valid). SLIM_DEV_BADPAGE: rows of that
+ * page are not written, and outputs that would read it are zero. Queries, and
+ * keys and values of attended rows, must be finite; whatever lies in the pages
+ * behind a sequence's rows is never used.
  *
  * Return codes of all calls: SLIM_EINVAL for a null or misaligned pointer
  * (16 bytes), a size out of range or head counts that do not divide;
@@ -342,7 +346,7 @@ typedef struct slim_paged_cache {
  *            SLIM_DEV_OVERFLOW
  *   q_out    [rows][Hq][dh] bf16 contiguous: the rotated queries; NULL exactly
  *            when q is. May equal q where q is contiguous.
- *   Hq       query heads (ignored without q)
+ *   Hq       query heads, a multiple of Hkv and at most 8192 (ignored without q)
  *   rows     rows of the packed arrays; 0 returns SLIM_OK and launches nothing
  */
 int slim_mha_paged_append(const slim_paged_cache* cache, const void* q, int64_t q_stride, const void* k,
@@ -372,7 +376,7 @@ int slim_mha_paged_gather(const slim_paged_cache* cache, const int32_t* starts, 
  *   q           [B][Hq][dh] bf16, row stride q_stride elements (rotated)
  *   rows_extra  1 after slim_mha_paged_append of the step's row, 0 to attend
  *               over lens[b] rows only (a fixed cache)
- *   Hq          a multiple of Hkv
+ *   Hq          a multiple of Hkv, at most 8192
  *   t_hint      host-side estimate of the longest attended length, used only
  *               to choose how work is split (<= 0 means cap)
  *   out         [B][Hq][dh] bf16 contiguous; zero for a sequence that was
@@ -392,10 +396,10 @@ int slim_mha_paged_decode(const slim_paged_cache* cache, const void* q, int64_t 
  * Whole prompts, chunks behind cached rows and a few proposed tokens alike.
  *
  *   q          [rows][Hq][dh] bf16, row stride q_stride elements (rotated)
- *   Hq         a multiple of Hkv, at most 128·Hkv
+ *   Hq         a multiple of Hkv, at most 128·Hkv and 8192
  *   t_hint     host-side estimate of the longest lens[b] + new rows, used only
- *              to choose how work is split (<= 0 means cap). The workspace call takes the
- *              same value.
+ *              to choose how work is split (<= 0 means cap). The workspace call
+ *              takes the same value.
  *   out        [rows][Hq][dh] bf16 contiguous
  *   workspace  >= slim_mha_paged_prefill_workspace_bytes(...), 256-byte aligned
  *              (may be NULL where that is 0)

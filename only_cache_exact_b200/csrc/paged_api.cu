@@ -14,6 +14,8 @@ void set_last_launch_count(int n);
 namespace {
 
 constexpr int64_t kInt32Max = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxCap = int64_t(1) << 30;   // a position and the tile behind it fit in int32
+constexpr int64_t kMaxRows = int64_t(1) << 35;  // the 16-row tiles of all sequences are counted in 32 bits
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -26,8 +28,8 @@ int check_cache(const slim_paged_cache* c) {
   if (c->dtype == SLIM_F32 || (c->dh != 64 && c->dh != 128) || c->B > kPagedMaxB ||
       (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128))
     return SLIM_EUNSUPPORTED;
-  if (c->num_pages > kInt32Max / (static_cast<int64_t>(c->Hkv) * c->page) ||
-      static_cast<int64_t>(c->max_pages) * c->page > kInt32Max)
+  const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page;
+  if (c->num_pages > kInt32Max / (static_cast<int64_t>(c->Hkv) * c->page) || cap > kMaxCap || cap * c->B > kMaxRows)
     return SLIM_EINVAL;
   if (c->dtype == SLIM_E4M3 && (!c->kscale || !c->vscale || !aligned(c->kscale, 4) || !aligned(c->vscale, 4)))
     return SLIM_EINVAL;
@@ -76,6 +78,7 @@ int slim_mha_paged_append(const slim_paged_cache* cache, const void* q, int64_t 
   if (!check_rows(k, k_stride, cache->Hkv, cache->dh) || !check_rows(v, v_stride, cache->Hkv, cache->dh) ||
       (q && (!check_rows(q, q_stride, Hq, cache->dh) || !aligned(q_out, 16))))
     return SLIM_EINVAL;
+  if (q && q == q_out && q_stride != static_cast<int64_t>(Hq) * cache->dh) return SLIM_EINVAL;
   if (rot < 0 || rot > cache->dh || rot % 16 || (rot > 0) != (cosines != nullptr) || !cosines != !sines)
     return SLIM_EINVAL;
   if (rot > 0 && (n_pos < 1 || !aligned(cosines, 16) || !aligned(sines, 16))) return SLIM_EINVAL;
@@ -112,7 +115,8 @@ int slim_mha_paged_decode(const slim_paged_cache* cache, const void* q, int64_t 
   if (!lens || !aligned(lens, 4) || !out || !aligned(out, 16) || !dev_status) return SLIM_EINVAL;
   if (rows_extra != 0 && rows_extra != 1) return SLIM_EINVAL;
   if (Hq < 1 || Hq > 8192 || Hq % cache->Hkv || !check_rows(q, q_stride, Hq, cache->dh)) return SLIM_EINVAL;
-  if (!workspace || !aligned(workspace, 256) || ws_bytes < paged_rows_ws_bytes(*cache, Hq / cache->Hkv)) return SLIM_EWORKSPACE;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < paged_rows_ws_bytes(*cache, Hq / cache->Hkv))
+    return SLIM_EWORKSPACE;
   int launches = 0;
   const cudaError_t e = launch_paged_rows(*cache, q, q_stride, nullptr, lens, cache->B, 1, rows_extra, Hq, t_hint, out,
                                           workspace, dev_status, static_cast<cudaStream_t>(stream), &launches);
@@ -121,7 +125,7 @@ int slim_mha_paged_decode(const slim_paged_cache* cache, const void* q, int64_t 
 
 size_t slim_mha_paged_prefill_workspace_bytes(const slim_paged_cache* cache, int Hq, int64_t rows, int64_t max_new,
                                               int64_t t_hint) {
-  if (check_cache(cache) != SLIM_OK || Hq < 1 || Hq % cache->Hkv || Hq / cache->Hkv > 128 || rows < 1 ||
+  if (check_cache(cache) != SLIM_OK || Hq < 1 || Hq > 8192 || Hq % cache->Hkv || Hq / cache->Hkv > 128 || rows < 1 ||
       rows > kInt32Max || max_new < 0)
     return 0;
   return paged_prefill_ws_bytes(*cache, Hq, rows, max_new == 0 ? rows : std::min(max_new, rows), t_hint);

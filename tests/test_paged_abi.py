@@ -32,6 +32,7 @@ BAD_CACHES = [
     (dict(dtype=7), "EINVAL"), (dict(B=0), "EINVAL"), (dict(Hkv=0), "EINVAL"), (dict(Hkv=1025), "EINVAL"),
     (dict(page=0), "EINVAL"), (dict(max_pages=0), "EINVAL"), (dict(num_pages=0), "EINVAL"),
     (dict(num_pages=1 << 22), "EINVAL"), (dict(max_pages=1 << 25), "EINVAL"), (dict(num_pages=1 << 62), "EINVAL"),
+    (dict(page=16, max_pages=(1 << 26) + 1, B=1), "EINVAL"), (dict(max_pages=1 << 21, B=300), "EINVAL"),
     (dict(dtype=0), "EUNSUPPORTED"), (dict(dh=96), "EUNSUPPORTED"), (dict(page=48), "EUNSUPPORTED"),
     (dict(page=256), "EUNSUPPORTED"), (dict(B=4097), "EUNSUPPORTED"),
 ]
@@ -86,7 +87,7 @@ def test_null_cache(S):
     dict(q=None), dict(k=F + 2), dict(q_out=F + 4), dict(ks=1016), dict(vs=1028), dict(qs=4088), dict(rot=-16),
     dict(rot=8), dict(rot=144), dict(rot=0), dict(cos=None), dict(sin=None), dict(cos=None, sin=None),
     dict(cos=F + 4), dict(n_pos=0), dict(inter=2), dict(rows=-1), dict(max_new=-1), dict(Hq=0), dict(Hq=33),
-    dict(rows=1 << 31), dict(starts=F + 2),
+    dict(rows=1 << 31), dict(starts=F + 2), dict(Hq=8200, qs=1 << 21), dict(qs=8192, q_out=F),
 ])
 def test_append_refusals(S, kw):
     assert append(S, **kw) == S.SLIM_EINVAL
@@ -131,6 +132,8 @@ def test_prefill_workspace(S):
     decode = S.raw_lib().slim_mha_paged_decode_workspace_bytes
     assert size(cache(S), 8, 7, 1, 0) == decode(cache(S), 8)  # one row of a key head: the same kernel
     assert size(cache(S), 31, 7, 0, 0) == 0 and size(cache(S), 32, 0, 0, 0) == 0
+    assert size(cache(S, Hkv=1024), 9 * 1024, 20, 0, 0) == 0  # as the call refuses them
+    assert prefill(S, cache(S, Hkv=1024), Hq=9 * 1024, qs=1 << 21) == S.SLIM_EINVAL
     assert size(cache(S), 32, 20, 0, 1 << 40) == size(cache(S), 32, 20, 0, 0)  # a hint past the capacity is the capacity
 
 

@@ -328,3 +328,73 @@ def test_no_rows(S):
     S.slim_mha_paged_prefill(st.cache, e, st.starts([0, 0]), st.lens, e,
                              torch.empty(0, dtype=torch.uint8, device="cuda"), st.status)
     assert S.slim_last_launch_count() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(S, kind):
+    """Both attentions over pools of more than 2^32 bytes whose used pages lie at the far end: as over a copy of those
+    pages in small pools, bit by bit."""
+    Hkv, Hq, dh, page = 64, 128, 128, 128
+    per = Hkv * dh * page * (2 if kind == "bf16" else 1)
+    num = (1 << 32) // per + 4
+    dt = torch.bfloat16 if kind == "bf16" else torch.float8_e4m3fn
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    far = [num - 1, num - 3, num - 2, num - 4]
+    big = [torch.empty(num, Hkv, page, dh, dtype=dt, device="cuda") for _ in range(2)]
+    small = [torch.randn(4, Hkv, page, dh, device="cuda", generator=gen).to(dt) for _ in range(2)]
+    for w in (0, 1):
+        for i, p in enumerate(far):
+            big[w][p] = small[w][i]
+    sc = [[None, None], [None, None]]
+    if kind == "e4m3":
+        sc = [[torch.ones(n, Hkv, device="cuda") for _ in range(2)] for n in (num, 4)]
+    tables = [torch.tensor([f[:3], f[3:] * 3], dtype=torch.int32, device="cuda") for f in (far, [0, 1, 2, 3])]
+    caches = [S.PagedKV(p[0], p[1], t, s[0], s[1]) for p, t, s in zip((big, small), tables, sc)]
+    lens = torch.tensor([330, 100], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    n = [40, 25]
+    q = torch.randn(sum(n), Hq, dh, device="cuda", generator=gen).bfloat16()
+    starts = torch.tensor([0, 40, 65], dtype=torch.int32, device="cuda")
+    got = []
+    for c in caches:
+        o, d = torch.zeros_like(q), torch.zeros_like(q[:2])
+        S.slim_mha_paged_prefill(c, q, starts, lens, o, S.alloc_paged_prefill_workspace(c, Hq, 65, 40), status, max_new=40)
+        S.slim_mha_paged_decode(c, q[:2], lens, d, S.alloc_paged_decode_workspace(c, Hq), status, rows_extra=0)
+        got.append((o, d))
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and torch.isfinite(a).all() and (a != 0).any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_calls_side_by_side(S, kind):
+    """A prompt chunk, single tokens and a read-back of one cache on three streams at once, each with its own
+    workspace, over and over: the results of the calls one after another."""
+    st = PagedState(S, kind, 2, 128, 32, [900, 1200], [900, 1200], seed=31)
+    n = [150, 70]
+    st.lens = torch.tensor([750, 1130], dtype=torch.int32, device="cuda")
+    q, q1, starts, first = st.rows(n, 8), st.rows([1, 1], 8), st.starts(n), st.lens.clone()
+    ws, ws1 = S.alloc_paged_prefill_workspace(st.cache, 8, 220, 150), S.alloc_paged_decode_workspace(st.cache, 8)
+
+    def outs():
+        return [torch.zeros_like(q), torch.zeros_like(q1)] + [torch.zeros_like(q[:, :2]).contiguous() for _ in range(2)]
+
+    def calls(o, streams):
+        S.slim_mha_paged_prefill(st.cache, q, starts, st.lens, o[0], ws, st.status, max_new=150, stream=streams[0])
+        S.slim_mha_paged_decode(st.cache, q1, st.lens, o[1], ws1, st.status, rows_extra=0, stream=streams[1])
+        S.slim_mha_paged_gather(st.cache, first, starts, o[2], o[3], st.status, max_new=150, stream=streams[2])
+
+    want = outs()
+    calls(want, [None] * 3)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    rounds = [outs() for _ in range(6)]
+    torch.cuda.synchronize()
+    for o in rounds:
+        calls(o, streams)
+    torch.cuda.synchronize()
+    for o in rounds:
+        for a, b in zip(o, want):
+            assert torch.equal(a, b)
+    check(st, q, want[0], n, [750, 1130])
+    assert int(st.status.item()) == 0
