@@ -876,7 +876,8 @@ PfPlan pf_plan(const slim_paged_cache& c, int Hq, int64_t rows, int64_t max_new,
   // from the rows up to half a pair per sequence.
   const int sms = num_sms();
   const int64_t nk = (hint + kFK - 1) / kFK;
-  const int64_t some = std::min<int64_t>(static_cast<int64_t>(c.B) * f.pairs, rows / (2 * f.QPT) + (c.B + 1) / 2);
+  const int64_t some = std::min<int64_t>(static_cast<int64_t>(c.B) * f.pairs,
+                                         std::max(rows / (2 * f.QPT) + (c.B + 1) / 2, rows / max_new * f.pairs));
   const int64_t ctas = std::max<int64_t>(1, some) * c.Hkv;
   double best = 0;
   f.splits = 1;
