@@ -42,7 +42,7 @@ constexpr int kFQ = 128;  // rows of a tile
 constexpr int kFK = 128;  // keys of a tile
 constexpr uint32_t kFTmemPerTile = 256;  // S (and P over it) at columns 0..127, O at 128
 constexpr float kFLazyLog2 = 8.f;
-constexpr int kFSetup = 4;  // a CTA's fixed time in key tiles
+constexpr int kFSetup = 4;  // a CTA's fixed time (query, first S, output) in key tiles of about 2.2 us
 
 struct PagedPrefillParams {
   PagedView c;
@@ -64,9 +64,10 @@ struct PagedPrefillParams {
 template <bool E, int DHB>
 struct PfCfg {
   // Keys of a step, the unit of S, softmax and P·V. Halves of a key tile (e4m3) have a TMEM region each, so
-  // that S of the next tile's half runs under the softmax of this one's other half: 816 -> 749 us for the
-  // 16K chunk. In bf16 the 64-key S MMAs cost as much shared-memory bandwidth as 128-key ones (their A
-  // operand is read either way) and the whole tile is faster: 544 -> 514 us for the 8192-token prompt.
+  // that S of the next tile's half runs under the softmax of this one's other half: 622 us against 709 with
+  // whole tiles (4 chunks of 300 to 512 rows behind 16000, 32 query heads over 8 of 128). In bf16 the 64-key
+  // S MMAs cost as much shared-memory bandwidth as 128-key ones (their A operand is read either way) and the
+  // whole tile is faster: 495 us against 514 (a prompt of 8192 rows, 32 heads of 128).
   static constexpr int FH = E ? 64 : 128;
   static constexpr int HV = kFK / FH;                          // steps of a key tile
   static constexpr int kPart1 = FH == 128 ? 96 : 64;           // keys of P that are handed over first
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     const int pos = live ? len + qi : -1;  // a row without a query attends nothing
     float fq = p.scale_log2;
     // The warp's 32 query rows into the Q tile, zeros where there is none: LR lanes read one row, so that
-    // a load takes whole lines (a row per thread took 7,000 cycles at dh = 128, this 1,500).
+    // a load takes whole lines (1,500 cycles at dh = 128; a row per thread took 7,000).
     {
       constexpr int LR = DH / 8, RI = 32 / LR;  // lanes of a row, rows of a load
       const int c = lane % LR;
@@ -854,10 +855,13 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PagedPrefillPa
   for (int k = 0; k < PL; k += 2) dst[k / 2] = broken ? 0u : round_bf16x2(o[k] * inv, o[k + 1] * inv);
 }
 
-// Rows of a (sequence, key head) up to which the kernel of paged_decode.cu is taken: it streams the
-// cache near memory speed, where a 128-row tile here would be mostly empty.
-constexpr int kFFewRows = 32;
-bool pf_few(const slim_paged_cache& c, int Hq, int64_t max_new) { return max_new * (Hq / c.Hkv) <= kFFewRows; }
+// Rows of a (sequence, key head) up to which the kernel of paged_decode.cu is taken: it streams the cache
+// near memory speed, where a 128-row tile here would be mostly empty. Its work grows with every 8 rows, here
+// it does not. 16 rows, there and here: 58 and 77 us at dh = 128 (8 sequences of 8000 rows, 8 key heads,
+// bf16), 34 and 65 us at dh = 64. 32 rows: 88 and 75 us at dh = 128, 52 and 64 us at dh = 64.
+bool pf_few(const slim_paged_cache& c, int Hq, int64_t max_new) {
+  return max_new * (Hq / c.Hkv) <= (c.dh == 64 ? 32 : 16);
+}
 
 struct PfPlan {
   int G, QPT, pairs, splits;

@@ -117,9 +117,9 @@ def test_decode_refusals(S, kw, code):
     (dict(wsb=100), "EWORKSPACE"),
 ])
 def test_prefill_refusals(S, kw, code):
-    # both ways to run it need scratch: 7 rows of 4 heads take the few-row kernel, and 20 rows of 4 sequences over a
+    # both ways to run it need scratch: 4 rows of 4 heads take the few-row kernel, and 20 rows of 4 sequences over a
     # capacity of 1280 rows have too few CTAs, so that keys are split
-    for rows in (7, 20):
+    for rows in (4, 20):
         assert S.raw_lib().slim_mha_paged_prefill_workspace_bytes(cache(S), 32, rows, 0, 0) > 100
     assert prefill(S, **kw) == getattr(S, "SLIM_" + code)
 
