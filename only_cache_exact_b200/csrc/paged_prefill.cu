@@ -29,7 +29,8 @@
 //
 // Few rows behind a long cache leave most SMs without a CTA: the key tiles are
 // then cut into `splits` ranges, each CTA leaves (m, l, O), and
-// merge_prefill_kernel joins them.
+// merge_prefill_kernel joins them. Where all queries of a sequence fit one row
+// tile, an e4m3 cache's keys are divided between the two row tiles as well.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -54,9 +55,10 @@ struct PagedPrefillParams {
   int Hq, G, QPT;  // QPT = 128 / G queries of a tile
   uint32_t g_inv;  // ceil(2^16 / G): row / G = row * g_inv >> 16 for row < 128
   int pairs, splits;
+  int parts;     // partial results of a row: splits, twice as many with kTwo; 1: none
   __nv_bfloat16* out;
-  float* ws_o;   // [split][rows][Hq][dh], splits > 1
-  float* ws_ml;  // [split][rows][Hq][2]
+  float* ws_o;   // [part][rows][Hq][dh], parts > 1
+  float* ws_ml;  // [part][rows][Hq][2]
   int32_t* status;
   float scale_log2;
 };
@@ -151,7 +153,12 @@ __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <bool E, int DHB>
+// kTwo (e4m3): no sequence has more queries than a row tile. Both row tiles then hold them, and take the CTA's
+// even and odd key tiles; their (m, l, O) are joined like those of splits. One row tile alone waits on its own
+// chain of S, softmax and P·V: 8 queries of 64 heads over 8 of 128 in 8 sequences of 8000 rows 78 us, this 60;
+// 16 sequences of 3000, 32 heads, 57 and 48. Over bf16 the rings have two stages at dh = 128, one for each row
+// tile here, and the next load is always waited for: 76 us, and 81 with this.
+template <bool E, int DHB, bool kTwo>
 __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const PagedPrefillParams p) {
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   const int nqt = (n + p.QPT - 1) / p.QPT;
   if (2 * pair >= nqt) return;
   // tile t of the pair holds queries q0 .. q0 + QPT - 1; a negative q0 is an absent tile
-  auto tile_q0 = [&](int t) { return (nqt - 2 * (pair + 1) + t) * p.QPT; };
+  auto tile_q0 = [&](int t) { return kTwo ? 0 : (nqt - 2 * (pair + 1) + t) * p.QPT; };
   auto tile_keys = [&](int t) {  // key tiles that tile t attends
     const int q0 = tile_q0(t);
     return q0 < 0 ? 0 : (len + min(q0 + p.QPT, n) - 1) / kFK + 1;
@@ -215,11 +222,15 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   const int kt0 = static_cast<int>(static_cast<int64_t>(split) * nk_all / p.splits);
   const int kt1 = static_cast<int>(static_cast<int64_t>(split + 1) * nk_all / p.splits);
   const int nkt = kt1 - kt0;
+  // key tile of the CTA that is tile t's j-th
+  auto key_tile = [](int t, int j) { return kTwo ? 2 * j + t : j; };
   // steps of this split that tile t attends
   auto tile_steps = [&](int t) {
     const int q0 = tile_q0(t);
     const int all = q0 < 0 ? 0 : (len + min(q0 + p.QPT, n) - 1) / FH + 1;
-    return max(0, min(HV * kt1, all) - HV * kt0);
+    const int steps = max(0, min(HV * kt1, all) - HV * kt0);
+    // the last key tile, which may have one step only, is that of tile (nkt - 1) & 1
+    return !kTwo ? steps : HV * ((nkt + 1 - t) >> 1) - (((nkt - 1) & 1) == t ? HV * nkt - steps : 0);
   };
 
   if (warp == 0 && lane == 0) {
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       const uint32_t tmem_t = tmem + t * kFTmemPerTile;
       const int steps = tile_steps(t);
       // key tiles that only this row tile reads: it releases them for both
-      const int alone = t == 1 ? (tile_steps(0) + HV - 1) / HV : 0x7fffffff;
+      const int alone = kTwo ? 0 : t == 1 ? (tile_steps(0) + HV - 1) / HV : 0x7fffffff;
       const int first_fix = E ? 0x7fffffff : max(0, Lz / kFK - kt0);  // first key tile with rows past Lz
       const bool lead = elect_one();
       bool ok = warp_wait(qbar, 0u, p.status);
@@ -425,14 +436,23 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         }
         return true;
       };
-      if (ok && steps > 0) {
-        ok = warp_wait(&kfull[0], 0u, p.status);
-        for (int u = 0; ok && u < min(HV, steps); ++u) issue_s(u, 0);
-      }
-      int sv = 0, sk = 1;  // V stage of the key tile, K stage of the next one
+      constexpr int kStep = kTwo ? 2 : 1;  // from one of its key tiles to the next
+      int sv = kTwo ? t : 0, sk = sv;      // V stage of the key tile, K stage of the next one
       uint32_t phv = 0u, phk = 0u;
+      auto next_stage = [](int& s, uint32_t& ph, int ring) {
+        s += kStep;
+        if (s >= ring) {
+          s -= ring;
+          ph ^= 1u;
+        }
+      };
+      if (ok && steps > 0) {
+        ok = warp_wait(&kfull[sk], 0u, p.status);
+        for (int u = 0; ok && u < min(HV, steps); ++u) issue_s(u, sk);
+      }
+      next_stage(sk, phk, NK);
       for (int u = 0; ok && u < steps; ++u) {
-        const int hf = HV == 2 ? u & 1 : 0, i = u / HV;
+        const int hf = HV == 2 ? u & 1 : 0, i = key_tile(t, u / HV);
         if (hf == 0) {
           ok = warp_wait(&vfull[sv], phv, p.status) && (u + HV >= steps || warp_wait(&kfull[sk], phk, p.status));
           if (!ok) break;
@@ -455,14 +475,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         if (!(ok = issue_pv(u, sv))) break;
         if (u + HV < steps) issue_s(u + HV, sk);  // overwrites the P that the P·V above reads: issued after it
         if (hf == HV - 1) {
-          if (++sv == NV) {
-            sv = 0;
-            phv ^= 1u;
-          }
-          if (++sk == NK) {
-            sk = 0;
-            phk ^= 1u;
-          }
+          next_stage(sv, phv, NV);
+          next_stage(sk, phk, NK);
         }
       }
       // also after a failure: the output barrier covers every MMA issued
@@ -597,8 +611,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     bool ok = true;
 #pragma unroll 1
     for (int u = 0; u < steps; ++u) {
-      const int i = u / HV, hf = HV == 2 ? u & 1 : 0;
-      const uint32_t ph = static_cast<uint32_t>(i) & 1u, tsh = ts + lrow + static_cast<uint32_t>(hf * FH);
+      const int i = key_tile(t, u / HV), hf = HV == 2 ? u & 1 : 0;
+      const uint32_t ph = static_cast<uint32_t>(u / HV) & 1u, tsh = ts + lrow + static_cast<uint32_t>(hf * FH);
       const int k0 = (kt0 + i) * kFK + hf * FH;
       if (!warp_wait(&sfull[2 * t + hf], ph, p.status)) {
         ok = false;
@@ -757,7 +771,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       }
       __syncwarp();
     };
-    if (p.splits == 1) {
+    if (!kTwo && p.splits == 1) {
       if (q0 >= 0) {
         const float inv = !got || broken || l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -781,7 +795,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         }
       }
     } else if (q0 >= 0) {
-      const int64_t first = static_cast<int64_t>(split) * p.rows * p.Hq;
+      const int64_t first = static_cast<int64_t>(kTwo ? 2 * split + t : split) * p.rows * p.Hq;
       if (live) {
         const int64_t prow = first + (static_cast<int64_t>(r.row0) + qi) * p.Hq + head;
         p.ws_ml[prow * 2] = steps > 0 && got ? m : -INFINITY;
@@ -816,7 +830,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   }
 }
 
-// Joins the splits of each (row, head): one warp each.
+// Joins the parts of each (row, head): one warp each.
 template <int DH>
 __global__ void __launch_bounds__(256) merge_prefill_kernel(const PagedPrefillParams p) {
   pdl_launch_dependents();
@@ -829,14 +843,14 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PagedPrefillPa
   const int64_t row = static_cast<int64_t>(r.row0) * p.Hq + item, step = p.rows * p.Hq;
   float M = -INFINITY;
   bool broken = false;
-  for (int s = 0; s < p.splits; ++s) {
+  for (int s = 0; s < p.parts; ++s) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + s * step + row);
     M = fmaxf(M, ml.x);
     broken |= ml.y < 0.f;
   }
   constexpr int PL = DH / 32;  // columns of a lane
   float o[PL] = {}, L = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
+  for (int s = 0; s < p.parts; ++s) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + s * step + row);
     if (ml.x == -INFINITY) continue;
     const float f = pf_ex2(ml.x - M);
@@ -857,14 +871,16 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PagedPrefillPa
 
 // Rows of a (sequence, key head) up to which the kernel of paged_decode.cu is taken: it streams the cache
 // near memory speed, where a 128-row tile here would be mostly empty. Its work grows with every 8 rows, here
-// it does not. 16 rows, there and here: 58 and 77 us at dh = 128 (8 sequences of 8000 rows, 8 key heads,
-// bf16), 34 and 65 us at dh = 64. 32 rows: 88 and 75 us at dh = 128, 52 and 64 us at dh = 64.
+// it does not. 8 sequences of 8000 rows, 8 key heads, there and here. 16 rows: dh = 128 58 and 77 us (bf16), 46
+// and 60 (e4m3); dh = 64 34 and 65, 37 and 53. 32 rows: dh = 128 88 and 75, 87 and 60; dh = 64 52 and 64, 57
+// and 54 (e4m3, 64 sequences of 500: 45 and 58).
 bool pf_few(const slim_paged_cache& c, int Hq, int64_t max_new) {
   return max_new * (Hq / c.Hkv) <= (c.dh == 64 ? 32 : 16);
 }
 
 struct PfPlan {
   int G, QPT, pairs, splits;
+  bool two;
   size_t o_bytes, ml_bytes;
 };
 size_t pf_up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -885,25 +901,29 @@ PfPlan pf_plan(const slim_paged_cache& c, int Hq, int64_t rows, int64_t max_new,
   const int64_t ctas = std::max<int64_t>(1, some) * c.Hkv;
   double best = 0;
   f.splits = 1;
-  for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, nk / 4)); ++s) {
-    const double waves = static_cast<double>((ctas * s + sms - 1) / sms);
-    const double cost = waves * (static_cast<double>(nk) / s + kFSetup + (s > 1 ? 2 : 0));
-    if (s == 1 || cost < 0.95 * best) {
-      best = cost;
-      f.splits = static_cast<int>(s);
+  f.two = false;
+  for (int two = 0; two <= (c.dtype == SLIM_E4M3 && max_new <= f.QPT ? 1 : 0); ++two)
+    for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, nk / 4)); ++s) {
+      const double waves = static_cast<double>((ctas * s + sms - 1) / sms);
+      const double cost = waves * (static_cast<double>(nk) / (s * (two ? 2 : 1)) + kFSetup + (s > 1 || two ? 2 : 0));
+      if ((s == 1 && !two) || cost < 0.95 * best) {
+        best = cost;
+        f.splits = static_cast<int>(s);
+        f.two = two != 0;
+      }
     }
-  }
-  const size_t items = f.splits > 1 ? static_cast<size_t>(f.splits) * rows * Hq : 0;
+  const int parts = f.splits * (f.two ? 2 : 1);
+  const size_t items = parts > 1 ? static_cast<size_t>(parts) * rows * Hq : 0;
   f.o_bytes = pf_up256(items * c.dh * 4);
   f.ml_bytes = pf_up256(items * 8);
   return f;
 }
 
-template <bool E, int DHB>
+template <bool E, int DHB, bool kTwo>
 cudaError_t launch_pf(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedPrefillParams& p, cudaStream_t st,
                       int* launches) {
   using C = PfCfg<E, DHB>;
-  auto kern = paged_prefill_kernel<E, DHB>;
+  auto kern = paged_prefill_kernel<E, DHB, kTwo>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem, done);
   if (e != cudaSuccess) return e;
@@ -920,7 +940,7 @@ cudaError_t launch_pf(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pa
   e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
   if (e != cudaSuccess) return e;
   if (launches) ++*launches;
-  if (p.splits == 1) return cudaSuccess;
+  if (p.parts == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg2 = cfg;
   cfg2.gridDim = dim3(static_cast<unsigned>((p.max_new * p.Hq + 7) / 8), static_cast<unsigned>(p.c.B), 1);
   cfg2.blockDim = dim3(256, 1, 1);
@@ -965,6 +985,7 @@ cudaError_t launch_paged_prefill(const slim_paged_cache& c, const void* q, int64
   p.g_inv = (65536u + static_cast<uint32_t>(f.G) - 1u) / static_cast<uint32_t>(f.G);
   p.pairs = f.pairs;
   p.splits = f.splits;
+  p.parts = f.splits * (f.two ? 2 : 1);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + f.o_bytes);
@@ -976,14 +997,17 @@ cudaError_t launch_paged_prefill(const slim_paged_cache& c, const void* q, int64
     if (!encode_tmap_2d_bf16(&kmap, c.kpages, c.dh, lines, static_cast<uint64_t>(c.dh) * 2u, 64, c.page, true) ||
         !encode_tmap_2d_bf16(&vmap, c.vpages, c.dh, lines, static_cast<uint64_t>(c.dh) * 2u, 64, c.page, true))
       return cudaErrorInvalidValue;
-    return c.dh == 64 ? launch_pf<false, 1>(kmap, vmap, p, st, launches)
-                      : launch_pf<false, 2>(kmap, vmap, p, st, launches);
+    return c.dh == 64 ? launch_pf<false, 1, false>(kmap, vmap, p, st, launches)
+                      : launch_pf<false, 2, false>(kmap, vmap, p, st, launches);
   }
   // e4m3 keys go to the MMA as they are: whole rows, in the swizzle of their length
   if (!encode_tmap_2d_u8(&kmap, c.kpages, c.dh, static_cast<uint64_t>(c.num_pages) * c.Hkv * c.page, c.dh, c.page))
     return cudaErrorInvalidValue;
-  return c.dh == 64 ? launch_pf<true, 1>(kmap, vmap, p, st, launches)
-                    : launch_pf<true, 2>(kmap, vmap, p, st, launches);
+  if (f.two)
+    return c.dh == 64 ? launch_pf<true, 1, true>(kmap, vmap, p, st, launches)
+                      : launch_pf<true, 2, true>(kmap, vmap, p, st, launches);
+  return c.dh == 64 ? launch_pf<true, 1, false>(kmap, vmap, p, st, launches)
+                    : launch_pf<true, 2, false>(kmap, vmap, p, st, launches);
 }
 
 }  // namespace slim

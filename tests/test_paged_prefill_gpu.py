@@ -124,6 +124,46 @@ def test_long_cache_short_chunks(S, kind, dh, page, G):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dh,page,G", [(64, 16, 4), (128, 64, 4), (128, 128, 8), (128, 32, 1), (64, 64, 128)])
+@pytest.mark.parametrize("t_hint", [0, 900, 300])
+def test_one_row_tile(S, kind, dh, page, G, t_hint):
+    """No sequence has more queries than one row tile holds: over e4m3 two parts of its keys run side by side in a
+    CTA, with and without a split over CTAs, among them parts and splits that have no key tile."""
+    q_tile = 128 // G
+    cached = [5000, 3, 2047, 0, 640, 255, 60]
+    new = [q_tile, min(5, q_tile), 1, q_tile, (q_tile + 1) // 2, 1, min(6, q_tile)]
+    total = [a + n for a, n in zip(cached, new)]
+    st = PagedState(S, kind, 2, dh, page, total, total, seed=34)
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows(new, 2 * G, 2.0)
+    out = run(S, st, q, new, cached, max_new=q_tile, t_hint=t_hint)
+    assert S.slim_last_launch_count() == (1 if t_hint == 300 else 2) and int(st.status.item()) == 0
+    check(st, q, out, new, cached)
+    assert torch.equal(out, run(S, st, q, new, cached, max_new=q_tile, t_hint=t_hint))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("t_hint", [0, 900])
+def test_one_row_tile_skipped(S, kind, t_hint):
+    """The same with bad lengths and with pages outside the pool, in a key tile of either part."""
+    cached, new = [3, 9, 600, 700, 640], [10, 10, 16, 10, 7]
+    total = [a + n for a, n in zip(cached, new)]
+    st = PagedState(S, kind, 2, 128, 16, total, total, seed=35)
+    cap = st.cache.cap
+    st.table[2, 38] = -1       # positions 608..623
+    st.table[3, 7] = 1 << 30   # positions 112..127, in the first key tile
+    st.table[4, 10] = -5       # positions 160..175, in the second
+    lens = torch.tensor([-1, cap - 2, 600, 700, 640], dtype=torch.int32, device="cuda")
+    q = st.rows(new, 8)
+    out = run(S, st, q, new, cached, max_new=16, t_hint=t_hint, lens=lens)
+    assert int(st.status.item()) == S.SLIM_DEV_BADLEN | S.SLIM_DEV_OVERFLOW | S.SLIM_DEV_BADPAGE
+    assert (out[:20] == 0).all() and (out[28:] == 0).all()
+    K, V = (st.oracle[w].read(st.table_h[2], 608) for w in (0, 1))
+    o, A, D = P.attend(f64(q[20:28]), K, V, [600 + j for j in range(8)])
+    assert (np.abs(f64(out[20:28]) - o) <= bound(kind, 128, o, A, D)).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("Hq,Hkv,dh,page,new", [
     (3, 3, 64, 16, [5, 0, 8, 1, 2]), (6, 3, 128, 32, [4, 1, 0, 3, 2]), (4, 2, 64, 64, [8, 7, 1, 5, 0]),
     (4, 1, 128, 128, [4, 4, 4, 3, 1]), (8, 1, 64, 32, [1, 4, 3, 2, 4]), (32, 1, 128, 16, [1, 1, 0, 1, 1]),
