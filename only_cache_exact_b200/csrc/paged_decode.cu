@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kDRings = 192 * 1024;    // bytes of a CTA's rings
 constexpr int kDMergeScan = 256;       // sequences up to which the merge kernel takes the line's offsets from lens itself
+constexpr int kDWide = 3;              // CTAs per (sequence, head group) from which the wide merge is taken
 constexpr float kDLazyLog2 = 8.f;      // a row's maximum follows once a score exceeds it by this much
 
 struct PagedDecodeParams {
@@ -751,7 +752,12 @@ __device__ __forceinline__ DecSlots dec_slots(I x0, I x1, I X, I grid) {
 // Joins the partials of one (sequence, head group) that more than one CTA (or a CTA's join and a
 // warp in whose share it ends) holds. Which slots those are follows from the plan alone; the loads of
 // a slot's maximum, sum and output go out together.
-template <int DH, int NT, int W>
+//
+// kWide: a CTA takes one row and its threads are 1024 / DH groups, each with a share of the slots, for calls
+// with many slots of few sequences. Whole decode calls without and with it, bf16, T = 16384, dh = 128: one
+// sequence of one key head and 8 query heads (148 CTAs each) 42 and 15 us, two of 32 heads (74 CTAs) 98 and
+// 22, one of 8 key heads (18) 25 and 21; 4 of 8000 rows (4.6) 31 and 30, 9 of 4000 (2) 32.3 and 32.5.
+template <int DH, int NT, int W, bool kWide>
 __global__ void __launch_bounds__(256) merge_paged_kernel(const PagedDecodeParams p, int grid) {
   constexpr int kHeads = 8 * NT;
   pdl_launch_dependents();
@@ -792,15 +798,15 @@ __global__ void __launch_bounds__(256) merge_paged_kernel(const PagedDecodeParam
   };
   const int kvh = hg / p.NG, r0g = (hg - kvh * p.NG) * kHeads;
   const int nh = min(kHeads, sq.n * p.G - r0g);
-  for (int i = threadIdx.x; i < nh * DH / 4; i += 256) {
-    const int hd = i / (DH / 4);
+  constexpr int kQuads = DH / 4, kGroups = kWide ? 256 / kQuads : 1;
+  const int first = kWide ? static_cast<int>(blockIdx.y) * kQuads + static_cast<int>(threadIdx.x) % kQuads : threadIdx.x;
+  const int g = kWide ? static_cast<int>(threadIdx.x) / kQuads : 0;
+  for (int i = first; i < nh * kQuads; i += kWide ? nh * kQuads : 256) {
+    const int hd = i / kQuads;
     float M = -INFINITY, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     bool broken = false;
-#pragma unroll 4
-    for (int k = 0; k < total; ++k) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot(k) * kHeads + hd);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(k) * kHeads * DH) + i);
+    auto join = [&](const float2 ml, const float4 v) {
       broken |= ml.y < 0.f;
       const float Mn = fmaxf(M, ml.x), ref = Mn == -INFINITY ? 0.f : Mn;
       const float a = ex2(M - ref), f = ex2(ml.x - ref);
@@ -810,13 +816,26 @@ __global__ void __launch_bounds__(256) merge_paged_kernel(const PagedDecodeParam
       O.y = fmaf(O.y, a, f * v.y);
       O.z = fmaf(O.z, a, f * v.z);
       O.w = fmaf(O.w, a, f * v.w);
+    };
+#pragma unroll 4
+    for (int k = g; k < total; k += kGroups)
+      join(__ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot(k) * kHeads + hd),
+           __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot(k) * kHeads * DH) + i));
+    if (kWide) {
+      __shared__ float4 s_o[256];
+      __shared__ float2 s_ml[256];
+      s_o[threadIdx.x] = O;
+      s_ml[threadIdx.x] = make_float2(M, broken ? -1.f : L);
+      __syncthreads();
+      if (g > 0) return;
+      for (int k = 1; k < kGroups; ++k) join(s_ml[k * kQuads + threadIdx.x], s_o[k * kQuads + threadIdx.x]);
     }
     const float r = broken || L == 0.f ? 0.f : 1.f / L;
     const uint2 y = broken ? make_uint2(0u, 0u)
                            : make_uint2(round_bf16x2(O.x * r, O.y * r), round_bf16x2(O.z * r, O.w * r));
     const int rr = r0g + hd, j = rr / p.G;
     reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(sq.row0) + j) * p.Hq + static_cast<int64_t>(kvh) * p.G +
-                                      (rr - j * p.G)) * DH)[i - hd * (DH / 4)] = y;
+                                      (rr - j * p.G)) * DH)[i - hd * kQuads] = y;
   }
 }
 
@@ -870,12 +889,14 @@ cudaError_t launch_dec(const PagedDecodeParams& p, cudaStream_t st, int* launche
   if (launches) ++*launches;
   if (!p.split) return cudaSuccess;
   cudaLaunchConfig_t cfg2 = {};
-  cfg2.gridDim = dim3(static_cast<unsigned>(p.c.B * p.HG), 1, 1);
+  const bool wide = p.c.B * p.HG * kDWide <= grid;
+  cfg2.gridDim = dim3(static_cast<unsigned>(p.c.B * p.HG), wide ? 8 * NT : 1, 1);
   cfg2.blockDim = dim3(256, 1, 1);
   cfg2.stream = st;
   cfg2.attrs = attr;
   cfg2.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg2, merge_paged_kernel<DH, NT, C::kWarps>, p, grid);
+  e = wide ? cudaLaunchKernelEx(&cfg2, merge_paged_kernel<DH, NT, C::kWarps, true>, p, grid)
+           : cudaLaunchKernelEx(&cfg2, merge_paged_kernel<DH, NT, C::kWarps, false>, p, grid);
   if (e == cudaSuccess && launches) ++*launches;
   return e;
 }
@@ -924,10 +945,11 @@ cudaError_t launch_paged_rows(const slim_paged_cache& c, const void* q, int64_t 
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(c.dh));
   const int64_t hint = t_hint > 0 ? std::min(t_hint, p.c.cap) : p.c.cap;
   // One CTA per work sequence, no merge, where that is one wave and the longest sequence, which the call then
-  // waits for, is short. bf16, 8 key heads of 128, whole and split: one sequence of 512 rows 7.8 and 9.3 us,
-  // 1024 10.7 and 10.5, 2048 16.1 and 12.6; 16 of 1024 15.6 and 20.4, of 2048 25.2 and 30.1 where all are
-  // that long.
-  p.split = !(static_cast<int64_t>(c.B) * d.HG <= num_sms() && hint <= 1024);
+  // waits for, is short. bf16, dh = 128, whole and split: one sequence of 8 key heads (4 query heads each), 512
+  // rows 7.9 and 10.1 us, 1024 10.6 and 10.4, 1536 13.4 and 11.1; 8 such sequences of 1024 rows 11.8 and 15.0, of
+  // 1536 14.7 and 18.6 where all are that long; two of one key head with 32 query heads, 384 rows 16.3 and 16.8,
+  // 1024 26 and 17.
+  p.split = !(static_cast<int64_t>(c.B) * d.HG <= num_sms() && hint <= (d.NT == 4 ? 512 : 1024));
   if (c.dtype == SLIM_E4M3)
     return c.dh == 64 ? launch_dec_nt<true, 64>(p, d.NT, st, launches) : launch_dec_nt<true, 128>(p, d.NT, st, launches);
   return c.dh == 64 ? launch_dec_nt<false, 64>(p, d.NT, st, launches) : launch_dec_nt<false, 128>(p, d.NT, st, launches);
