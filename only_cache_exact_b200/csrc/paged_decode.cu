@@ -755,8 +755,8 @@ __device__ __forceinline__ DecSlots dec_slots(I x0, I x1, I X, I grid) {
 //
 // kWide: a CTA takes one row and its threads are 1024 / DH groups, each with a share of the slots, for calls
 // with many slots of few sequences. Whole decode calls without and with it, bf16, T = 16384, dh = 128: one
-// sequence of one key head and 8 query heads (148 CTAs each) 42 and 15 us, two of 32 heads (74 CTAs) 98 and
-// 22, one of 8 key heads (18) 25 and 21; 4 of 8000 rows (4.6) 31 and 30, 9 of 4000 (2) 32.3 and 32.5.
+// sequence of one key head and 8 query heads (148 CTAs each) 42 and 15 us, one of 8 key heads (18) 25 and 21;
+// 4 of 8000 rows (4.6) 31 and 30, 9 of 4000 (2) 32.3 and 32.5.
 template <int DH, int NT, int W, bool kWide>
 __global__ void __launch_bounds__(256) merge_paged_kernel(const PagedDecodeParams p, int grid) {
   constexpr int kHeads = 8 * NT;
@@ -847,7 +847,11 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // R query rows at most share a (sequence, key head)'s keys.
 DecPlan dec_plan(const slim_paged_cache& c, int R) {
   DecPlan d;
-  d.NT = R <= 8 ? 1 : R <= 16 ? 2 : 4;
+  // A group of 8, 16 or 32 rows; more groups read the cache again (from L2, mostly). 32 rows at dh = 128 want more
+  // registers than there are: groups of 16 and 32, e4m3: 68 and 87 us (64 sequences of 8000 rows, one key head,
+  // 32 query heads), 17 and 23 (2 of 1000); bf16 92 and 89, 16 and 21. At dh = 64 32 rows pay: 155 and 114 us (64
+  // sequences of 1250, 20 key heads, 32 query heads each).
+  d.NT = R <= 8 ? 1 : R <= 16 || c.dh == 128 ? 2 : 4;
   d.NG = (R + 8 * d.NT - 1) / (8 * d.NT);
   d.HG = c.Hkv * d.NG;
   const size_t slots = static_cast<size_t>(num_sms()) * 2 * dec_warps(c.dtype == SLIM_E4M3, c.dh, d.NT);
@@ -910,9 +914,9 @@ size_t paged_rows_ws_bytes(const slim_paged_cache& c, int R) {
 
 template <bool E, int DH>
 static cudaError_t launch_dec_nt(const PagedDecodeParams& p, int NT, cudaStream_t st, int* launches) {
-  return NT == 1   ? launch_dec<E, DH, 1>(p, st, launches)
-         : NT == 2 ? launch_dec<E, DH, 2>(p, st, launches)
-                   : launch_dec<E, DH, 4>(p, st, launches);
+  if (NT == 1) return launch_dec<E, DH, 1>(p, st, launches);
+  if (DH == 128 || NT == 2) return launch_dec<E, DH, 2>(p, st, launches);
+  return launch_dec<E, DH, DH == 64 ? 4 : 2>(p, st, launches);
 }
 
 // starts == nullptr: one row per sequence, attending lens[b] + rows_extra keys; else the packed rows,
@@ -947,9 +951,9 @@ cudaError_t launch_paged_rows(const slim_paged_cache& c, const void* q, int64_t 
   // One CTA per work sequence, no merge, where that is one wave and the longest sequence, which the call then
   // waits for, is short. bf16, dh = 128, whole and split: one sequence of 8 key heads (4 query heads each), 512
   // rows 7.9 and 10.1 us, 1024 10.6 and 10.4, 1536 13.4 and 11.1; 8 such sequences of 1024 rows 11.8 and 15.0, of
-  // 1536 14.7 and 18.6 where all are that long; two of one key head with 32 query heads, 384 rows 16.3 and 16.8,
-  // 1024 26 and 17.
-  p.split = !(static_cast<int64_t>(c.B) * d.HG <= num_sms() && hint <= (d.NT == 4 ? 512 : 1024));
+  // 1536 14.7 and 18.6 where all are that long. More rows a group: two sequences of one key head with 32 query
+  // heads, 512 rows 10.6 and 12.3, 768 12.5 and 12.5, 1024 14.2 and 12.6.
+  p.split = !(static_cast<int64_t>(c.B) * d.HG <= num_sms() && hint <= (d.NT == 1 ? 1024 : 768));
   if (c.dtype == SLIM_E4M3)
     return c.dh == 64 ? launch_dec_nt<true, 64>(p, d.NT, st, launches) : launch_dec_nt<true, 128>(p, d.NT, st, launches);
   return c.dh == 64 ? launch_dec_nt<false, 64>(p, d.NT, st, launches) : launch_dec_nt<false, 128>(p, d.NT, st, launches);

@@ -44,7 +44,7 @@ def check(st, q, out, lens, extra):
 
 
 HEADS = [(4, 4, 64), (20, 20, 64), (8, 1, 128), (14, 2, 64), (12, 4, 128), (9, 1, 64), (16, 1, 128), (34, 2, 64),
-         (40, 8, 128)]
+         (40, 8, 128), (33, 1, 128), (70, 1, 64)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
