@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   uint64_t* vfixed = ofull + 2;    // [NV] bf16: V rows past the end are zeroed
   uint64_t* rfull = vfixed + NV;     // [NR] raw V landed
   uint64_t* rempty = rfull + NR;   // [NR] raw V converted
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rempty + NR);
+  uint64_t* turn = rempty + NR;    // [row tile][warp of it] the other row tile's exponentials of a step are done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
   int* s_bad = reinterpret_cast<int*>(tmem_slot + 1);  // first position whose page is outside the pool
   // e4m3: [key tile mod 8] scale of its pages if they share one (key scale, value exponent, whether), then
   // key scale and value exponent of each page. Written by the K producer before the tile's barrier.
@@ -252,6 +253,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       mbar_init(&sfull[t], 1);
       mbar_init(&pready[t], 4);
     }
+    for (int t = 0; t < 8; ++t) mbar_init(&turn[t], 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&pvdone[t], 1);
       mbar_init(&ofull[t], 1);
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     const int row = quarter * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lrow = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + t * kFTmemPerTile, tmem_o = ts + 128u;
-    const int q0 = tile_q0(t), steps = tile_steps(t);
+    const int q0 = tile_q0(t), steps = tile_steps(t), steps_other = tile_steps(1 - t);
     auto div_g = [&](int x) { return static_cast<int>((static_cast<uint32_t>(x) * p.g_inv) >> 16); };
     const int qi = q0 + div_g(row), head = h * p.G + row - div_g(row) * p.G;
     const bool live = q0 >= 0 && row < p.QPT * p.G && qi < n;
@@ -652,6 +654,18 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           }
         }
       };
+      // The two row tiles' warps on one scheduler take turns at the exponentials: while one has the unit to
+      // itself, the other does the rest of its step. Left alone they fall into step, both waiting for the unit
+      // and then both leaving it idle. Without and with turns: 595 and 561 us (e4m3, a prompt of 8192 rows, 32
+      // heads of 128), 536 and 523 (4 chunks of 400 behind 16000, 32 over 8 heads), bf16 507 and 488 (the same
+      // chunks), 54 and 51 (a prompt of 2048); the 8192 rows in bf16 run at the power limit either way, 505.
+      auto take_turn = [&]() {
+        if (t == 0 ? u >= 1 && u - 1 < steps_other : u < steps_other)
+          ok = ok && warp_wait(&turn[t * 4 + quarter], static_cast<uint32_t>(t == 0 ? u - 1 : u) & 1u, p.status);
+      };
+      auto pass_turn = [&]() {
+        if (lane == 0) mbar_arrive(&turn[(1 - t) * 4 + quarter]);
+      };
       // P of keys 32 q .. 32 q + 31 of the step to tensor memory; the sums of either half of them
       auto weights = [&](int q, float f, float e0, float e1, float& sum0, float& sum1) {
         uint32_t pk[16];
@@ -702,6 +716,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], sc[FH - 4 + k]);
         const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
         advance(mt + lvu);
+        take_turn();
         const float mm = m == -INFINITY ? 0.f : m;
         float e = lvu - mm;
         if (E && mt != -INFINITY && e < -60.f - mt) e = -60.f - mt;
@@ -713,6 +728,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           total += s0 + s1;
           if (C::kParts == 2 && 32 * (q + 1) == C::kPart1) hand_over(0);
         }
+        pass_turn();
         l += E ? total * pf_ex2(-mm - e) : total;
       } else {
         float lv[FH / 16], mg[FH / 16], top = -INFINITY;
@@ -730,6 +746,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           top = fmaxf(top, mg[g] + lv[g]);
         }
         advance(top);
+        take_turn();  // and on at once: this form has more work than exponentials
+        pass_turn();
         const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll
         for (int q = 0; q < FH / 32; ++q) {
