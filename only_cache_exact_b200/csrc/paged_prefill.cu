@@ -43,6 +43,7 @@ constexpr int kFQ = 128;  // rows of a tile
 constexpr int kFK = 128;  // keys of a tile
 constexpr uint32_t kFTmemPerTile = 256;  // S (and P over it) at columns 0..127, O at 128
 constexpr float kFLazyLog2 = 8.f;
+constexpr int kScaleSlot = 24;  // floats of a key tile's scales
 constexpr int kFSetup = 4;  // a CTA's fixed time (query, first S, output) in key tiles of about 2.2 us
 
 struct PagedPrefillParams {
@@ -187,8 +188,9 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   uint64_t* turn = rempty + NR;    // [row tile][warp of it] the other row tile's exponentials of a step are done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
   int* s_bad = reinterpret_cast<int*>(tmem_slot + 1);  // first position whose page is outside the pool
-  // e4m3: [key tile mod 8] scale of its pages if they share one (key scale, value exponent, whether), then
-  // key scale and value exponent of each page. Written by the K producer before the tile's barrier.
+  // e4m3: [key tile mod 8] for either half of the keys the scale of its pages if they share one (key scale,
+  // value exponent, whether), then key scale and value exponent of each page. Written by the K producer before
+  // the tile's barrier.
   float* s_scale = reinterpret_cast<float*>(bars + 64);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
@@ -311,17 +313,18 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         const int sk = i % NK;
         if (i >= NK && !warp_wait(&kempty[sk], static_cast<uint32_t>(i / NK - 1) & 1u, p.status)) break;
         if (E) {
-          const float lv_l = scale_log2(vs_l), ks0 = __shfl_sync(0xffffffffu, ks_l, 0), lv0 = __shfl_sync(0xffffffffu, lv_l, 0);
-          const bool one = __all_sync(0xffffffffu, lane >= npg || (ks_l == ks0 && lv_l == lv0));
-          float* sc = s_scale + (i & 7) * 20;
+          const float lv_l = scale_log2(vs_l);
+          float* sc = s_scale + (i & 7) * kScaleSlot;
           if (lane < 8) {
-            sc[4 + 2 * lane] = ks_l;
-            sc[5 + 2 * lane] = lv_l;
+            sc[8 + 2 * lane] = ks_l;
+            sc[9 + 2 * lane] = lv_l;
           }
-          if (lane == 0) {
-            sc[0] = ks0;
-            sc[1] = lv0;
-            sc[2] = one ? 1.f : 0.f;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int first = half * (ppt >> 1), last = ppt == 1 ? 1 : first + (ppt >> 1);  // pages of the half
+            const float ks0 = __shfl_sync(0xffffffffu, ks_l, first), lv0 = __shfl_sync(0xffffffffu, lv_l, first);
+            const bool one = __all_sync(0xffffffffu, lane < first || lane >= min(last, npg) || (ks_l == ks0 && lv_l == lv0));
+            if (lane == 0) *reinterpret_cast<float4*>(sc + 4 * half) = make_float4(ks0, lv0, one ? 1.f : 0.f, 0.f);
           }
           ks_l = scale_of(p.c.ks, id_next);
           vs_l = scale_of(p.c.vs, id_next);
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     }
     float m = -INFINITY, l = 0.f;
     float ksu = 1.f, lvu = 0.f;
-    bool uniform = true;  // one scale pair for all pages of the key tile
+    bool uniform = true;  // one scale pair for all pages of the step
     bool ok = true;
 #pragma unroll 1
     for (int u = 0; u < steps; ++u) {
@@ -691,9 +694,9 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[2 * t + k]);
       };
-      const float* sc_scale = s_scale + (i & 7) * 20;
-      if (E && hf == 0) {
-        const float4 w = *reinterpret_cast<const float4*>(sc_scale);
+      const float* sc_scale = s_scale + (i & 7) * kScaleSlot;
+      if (E) {
+        const float4 w = *reinterpret_cast<const float4*>(sc_scale + 4 * hf);
         ksu = w.x;
         lvu = w.y;
         uniform = w.z != 0.f;
@@ -735,8 +738,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
 #pragma unroll
         for (int g = 0; g < FH / 16; ++g) {
           const int pg = (hf * FH + g * 16) >> psh;
-          const float f = sc_scale[4 + 2 * pg] * fq;
-          lv[g] = sc_scale[5 + 2 * pg];
+          const float f = sc_scale[8 + 2 * pg] * fq;
+          lv[g] = sc_scale[9 + 2 * pg];
           mg[g] = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
