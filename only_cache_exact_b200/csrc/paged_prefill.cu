@@ -670,15 +670,14 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         if (lane == 0) mbar_arrive(&turn[(1 - t) * 4 + quarter]);
       };
       // P of keys 32 q .. 32 q + 31 of the step to tensor memory; the sums of either half of them
-      auto weights = [&](int q, float f, float e0, float e1, float& sum0, float& sum1) {
+      auto weights = [&](int q, float f0, float f1, float e0, float e1, float& sum0, float& sum1) {
         uint32_t pk[16];
         uint64_t s2[2] = {0ull, 0ull};
-        const uint64_t ff = pack2(f, f);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const float e = c < 8 ? e0 : e1;
+          const float f = c < 8 ? f0 : f1, e = c < 8 ? e0 : e1;
           float x0, x1;
-          unpack2(ffma2(pack2(sc[32 * q + 2 * c], sc[32 * q + 2 * c + 1]), ff, pack2(e, e)), x0, x1);
+          unpack2(ffma2(pack2(sc[32 * q + 2 * c], sc[32 * q + 2 * c + 1]), pack2(f, f), pack2(e, e)), x0, x1);
           const float a = pf_ex2(x0), bb = pf_ex2(x1);
           s2[c >> 3] = fadd2(s2[c >> 3], pack2(a, bb));
           pk[c] = E ? round_f16x2(a, bb) : round_bf16x2(a, bb);
@@ -727,30 +726,40 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < FH / 32; ++q) {
           float s0, s1;
-          weights(q, f, e, e, s0, s1);
+          weights(q, f, f, e, e, s0, s1);
           total += s0 + s1;
           if (C::kParts == 2 && 32 * (q + 1) == C::kPart1) hand_over(0);
         }
         pass_turn();
         l += E ? total * pf_ex2(-mm - e) : total;
       } else {
-        float lv[FH / 16], mg[FH / 16], top = -INFINITY;
+        float fg[FH / 16], lv[FH / 16], mg[FH / 16], top = -INFINITY;
+        const bool masked = __any_sync(0xffffffffu, k0 + FH - 1 > pos);
 #pragma unroll
         for (int g = 0; g < FH / 16; ++g) {
           const int pg = (hf * FH + g * 16) >> psh;
-          const float f = sc_scale[8 + 2 * pg] * fq;
+          fg[g] = sc_scale[8 + 2 * pg] * fq;
           lv[g] = sc_scale[9 + 2 * pg];
-          mg[g] = -INFINITY;
+        }
+        if (masked) {  // scaled first: a masked score is -inf also beside a NaN scale
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            sc[16 * g + c] = k0 + 16 * g + c <= pos ? sc[16 * g + c] * f : -INFINITY;  // after a NaN scale
-            mg[g] = fmaxf(mg[g], sc[16 * g + c]);
+          for (int g = 0; g < FH / 16; ++g) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              sc[16 * g + c] = k0 + 16 * g + c <= pos ? sc[16 * g + c] * fg[g] : -INFINITY;
+            fg[g] = 1.f;
           }
+        }
+#pragma unroll
+        for (int g = 0; g < FH / 16; ++g) {
+          float mx = fmax3(sc[16 * g], sc[16 * g + 1], sc[16 * g + 2]);
+#pragma unroll
+          for (int c = 3; c < 15; c += 2) mx = fmax3(mx, sc[16 * g + c], sc[16 * g + c + 1]);
+          mg[g] = fmaxf(mx, sc[16 * g + 15]) * fg[g];
           top = fmaxf(top, mg[g] + lv[g]);
         }
         advance(top);
-        take_turn();  // and on at once: this form has more work than exponentials
-        pass_turn();
+        take_turn();
         const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll
         for (int q = 0; q < FH / 32; ++q) {
@@ -761,10 +770,11 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
             e[k] = x == -INFINITY ? 0.f : lv[2 * q + k] - mm;
             if (e[k] < -60.f - x && x != -INFINITY) e[k] = -60.f - x;  // a NaN scale stays
           }
-          weights(q, 1.f, e[0], e[1], s2[0], s2[1]);
+          weights(q, fg[2 * q], fg[2 * q + 1], e[0], e[1], s2[0], s2[1]);
           l += s2[0] * pf_ex2(-mm - e[0]) + s2[1] * pf_ex2(-mm - e[1]);
           if (C::kParts == 2 && 32 * (q + 1) == C::kPart1) hand_over(0);
         }
+        pass_turn();
       }
       if (!ok) break;
       hand_over(HV == 2 ? hf : C::kParts - 1);
