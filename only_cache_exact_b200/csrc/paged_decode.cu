@@ -39,7 +39,7 @@ namespace slim {
 namespace {
 
 constexpr int kDRings = 192 * 1024;    // bytes of a CTA's rings
-constexpr int kDMergeScan = 256;       // sequences up to which the merge kernel takes the line's offsets from lens itself
+constexpr int kDMergeScan = 256;       // sequences up to which the merge kernel takes the line's offsets from lens
 constexpr int kDWide = 3;              // CTAs per (sequence, head group) from which the wide merge is taken
 constexpr float kDLazyLog2 = 8.f;      // a row's maximum follows once a score exceeds it by this much
 

@@ -67,10 +67,10 @@ struct PagedPrefillParams {
 template <bool E, int DHB>
 struct PfCfg {
   // Keys of a step, the unit of S, softmax and P·V. Halves of a key tile (e4m3) have a TMEM region each, so
-  // that S of the next tile's half runs under the softmax of this one's other half: 622 us against 709 with
-  // whole tiles (4 chunks of 300 to 512 rows behind 16000, 32 query heads over 8 of 128). In bf16 the 64-key
-  // S MMAs cost as much shared-memory bandwidth as 128-key ones (their A operand is read either way) and the
-  // whole tile is faster: 495 us against 514 (a prompt of 8192 rows, 32 heads of 128).
+  // that S of the next tile's half runs under the softmax of this one's other half: 522 us against 553 with
+  // whole tiles (4 chunks of 400 rows behind 16000, 32 query heads over 8 of 128). In bf16 the 64-key S MMAs
+  // cost as much shared-memory bandwidth as 128-key ones (their A operand is read either way) and the whole
+  // tile is faster: 504 us against 523 (a prompt of 8192 rows, 32 heads of 128).
   static constexpr int FH = E ? 64 : 128;
   static constexpr int HV = kFK / FH;                          // steps of a key tile
   static constexpr int kPart1 = FH == 128 ? 96 : 64;           // keys of P that are handed over first
@@ -79,7 +79,7 @@ struct PfCfg {
   static constexpr int NK = E ? 3 : DHB == 2 ? 2 : 4;          // stages of the K ring
   static constexpr int NV = DHB == 2 ? 2 : 4;                  // stages of the V ring the MMAs read
   static constexpr int NR = 2;                                 // stages of the raw V ring (e4m3)
-  static constexpr uint32_t kTile = kFK * DH * 2u;             // bytes of a 16-bit V tile, of a Q tile (16-bit, or e4m3 twice)
+  static constexpr uint32_t kTile = kFK * DH * 2u;             // bytes of a V tile, and of a Q tile (e4m3: two parts)
   static constexpr uint32_t kKTile = E ? kFK * DH : kTile;     // bytes of a K tile
   static constexpr uint32_t kRaw = E ? kFK * DH : 0u;          // bytes of a raw V tile
   static constexpr int kThreads = E ? 512 : 384;
@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           for (int half = 0; half < 2; ++half) {
             const int first = half * (ppt >> 1), last = ppt == 1 ? 1 : first + (ppt >> 1);  // pages of the half
             const float ks0 = __shfl_sync(0xffffffffu, ks_l, first), lv0 = __shfl_sync(0xffffffffu, lv_l, first);
-            const bool one = __all_sync(0xffffffffu, lane < first || lane >= min(last, npg) || (ks_l == ks0 && lv_l == lv0));
+            const bool one = __all_sync(0xffffffffu, lane < first || lane >= min(last, npg) ||
+                                                         (ks_l == ks0 && lv_l == lv0));
             if (lane == 0) *reinterpret_cast<float4*>(sc + 4 * half) = make_float4(ks0, lv0, one ? 1.f : 0.f, 0.f);
           }
           ks_l = scale_of(p.c.ks, id_next);
