@@ -57,6 +57,9 @@ CASES = [
     ("e4m3", 8, 8, 128, 128, [100, 0], [300, 129], 128, True),
     ("e4m3", 5, 5, 128, 64, [63, 1], [130, 63], 0, False),
     ("e4m3", 40, 8, 128, 16, [1, 14], [17, 100], 128, False),
+    ("e4m3", 2048, 1024, 64, 16, [3, 15], [14, 1], 64, True),
+    ("bf16", 8192, 64, 64, 16, [0, 15], [1, 1], 32, False),
+    ("e4m3", 2, 1, 64, 16, [i % 20 for i in range(4096)], [i % 3 % 2 for i in range(4096)], 64, False),
 ]
 
 

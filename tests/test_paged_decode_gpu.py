@@ -78,7 +78,8 @@ def test_ragged(S, kind, Hq, Hkv, dh, page, t_hint):
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("B,Hq,Hkv,dh,page,lo,hi", [(1, 4, 4, 64, 16, 9000, 9000), (1, 8, 1, 128, 128, 20000, 20000),
                                                     (300, 4, 2, 64, 16, 0, 90), (37, 8, 8, 128, 32, 100, 700),
-                                                    (3, 64, 4, 128, 64, 2000, 4000)])
+                                                    (3, 64, 4, 128, 64, 2000, 4000), (4096, 2, 1, 64, 16, 0, 20),
+                                                    (2, 8192, 1024, 64, 16, 30, 40), (1, 8192, 1, 128, 16, 100, 100)])
 def test_split_shapes(S, kind, B, Hq, Hkv, dh, page, lo, hi):
     """One long sequence over all CTAs, many short ones in one CTA, and mixtures."""
     rng = np.random.default_rng(5)

@@ -408,6 +408,22 @@ def test_offsets_past_32_bits(S, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,Hq,Hkv", [(4096, 2, 1), (4096, 40, 1), (2, 8192, 1024), (3, 8192, 64)])
+def test_most_sequences_and_heads(S, kind, B, Hq, Hkv):
+    """The largest batch and the most heads, in the few-row form and on row tiles."""
+    rng = np.random.default_rng(6)
+    cached, new = [int(x) for x in rng.integers(0, 24, size=B)], [int(x) for x in rng.integers(0, 4, size=B)]
+    new[-1] = 3
+    total = [a + n for a, n in zip(cached, new)]
+    st = PagedState(S, kind, Hkv, 64, 16, total, total, seed=36)
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows(new, Hq, 2.0)
+    out = run(S, st, q, new, cached, max_new=3)
+    assert int(st.status.item()) == 0
+    check(st, q, out, new, cached)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_calls_side_by_side(S, kind):
     """A prompt chunk, single tokens and a read-back of one cache on three streams at once, each with its own
     workspace, over and over: the results of the calls one after another."""
