@@ -884,7 +884,9 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PagedPrefillPa
   float o[PL] = {}, L = 0.f;
   for (int s = 0; s < p.parts; ++s) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + s * step + row);
-    if (ml.x == -INFINITY) continue;
+    // nothing attended in this part, whose O was not written then; a part over poisoned pages alone has no
+    // maximum either, but its l is NaN and stays
+    if (ml.x == -INFINITY && ml.y <= 0.f) continue;
     const float f = pf_ex2(ml.x - M);
     L = fmaf(f, ml.y, L);
     const float* src = p.ws_o + (s * step + row) * DH + lane * PL;

@@ -206,3 +206,34 @@ def test_steps_through_the_cache(S, kind):
         lens = [a + b for a, b in zip(lens, n)]
         st.lens += torch.tensor(n, dtype=torch.int32, device="cuda")
     assert int(st.status.item()) == 0 and st.lens.tolist() == lens
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("dh,Hq,Hkv,page", [(64, 4, 4, 16), (128, 8, 1, 16), (64, 20, 1, 64), (128, 64, 16, 128)])
+@pytest.mark.parametrize("at", [0, 2560, 4992])
+def test_poisoned_page_in_parts(S, which, dh, Hq, Hkv, page, at):
+    """A page whose scale is NaN, in the first, a middle or (alone, for small pages) the last warp's share of a split
+    sequence: NaN where it is attended, and the other sequence as it was."""
+    lens = [at + 5 if at == 4992 else 4992, 300]
+    st = PagedState(S, "e4m3", Hkv, dh, page, lens, [5000, 300], seed=17)
+    q = st.rows([1, 1], Hq)
+    ws = S.alloc_paged_decode_workspace(st.cache, Hq)
+    x, ok = st.rows([1], Hkv), st.rows([1], Hkv)
+    x[0, :, 5] = float("-inf")
+    starts = torch.tensor([0, 1, 1], dtype=torch.int32, device="cuda")
+    S.slim_mha_paged_append(st.cache, *((x, ok) if which == 0 else (ok, x)), starts,
+                            torch.tensor([at, 300], dtype=torch.int32, device="cuda"), st.status)
+    out = torch.full_like(q, 7.0)
+    S.slim_mha_paged_decode(st.cache, q, st.lens, out, ws, st.status, rows_extra=0)
+    assert S.slim_last_launch_count() == 2
+    torch.cuda.synchronize()
+    assert int(st.status.item()) == 0
+    assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
+    K, V = (st.oracle[w].read(st.table_h[1], 300) for w in (0, 1))
+    o, A, D = P.attend(f64(q[1:]), K, V, [299])
+    assert (np.abs(f64(out[1:]) - o) <= bound("e4m3", dh, o, A, D)).all()
+    if at:
+        lens2 = torch.tensor([at, 300], dtype=torch.int32, device="cuda")
+        S.slim_mha_paged_decode(st.cache, q, lens2, out, ws, st.status, rows_extra=0)
+        torch.cuda.synchronize()
+        check(st, q, out, [at, 300], 0)

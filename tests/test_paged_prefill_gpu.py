@@ -454,3 +454,52 @@ def test_calls_side_by_side(S, kind):
             assert torch.equal(a, b)
     check(st, q, want[0], n, [750, 1130])
     assert int(st.status.item()) == 0
+
+
+def poison(S, st, which, at):
+    """An infinite key (which = 0) or value at row `at` of sequence 0, which begins a page."""
+    assert at % st.page == 0
+    x, ok = st.rows([1], st.Hkv), st.rows([1], st.Hkv)
+    x[0, :, 5] = float("inf")
+    lens = torch.full_like(st.lens, at)
+    S.slim_mha_paged_append(st.cache, *((x, ok) if which == 0 else (ok, x)), st.starts([1]), lens, st.status)
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("dh,page,cached,new,at,cap,t_hint", [
+    (64, 16, 120, 28, 128, 4096, 0),      # the page begins the second key tile, which is a part of its own
+    (128, 16, 120, 20, 128, 4096, 0),
+    (64, 64, 120, 28, 128, 4096, 800),    # two ranges in one CTA: the second is that key tile
+    (64, 128, 600, 28, 256, 4096, 0),     # a whole key tile among the cached rows
+    (64, 16, 100, 60, 128, 4096, 0),      # more queries than a row tile: parts of CTAs alone
+    (128, 128, 500, 60, 512, 4096, 0),
+    (128, 128, 2048, 40, 128, 32768, 0),
+    (64, 128, 0, 30, 0, 4096, 0),         # nothing but the page
+])
+def test_poisoned_page_in_parts(S, which, dh, page, cached, new, at, cap, t_hint):
+    """Keys in parts that are joined, one of which holds nothing but the poisoned page for some rows: every output
+    that attends the page is NaN, the others are not touched."""
+    st = PagedState(S, "e4m3", 1, dh, page, [cached + new], [cap - page], seed=40)
+    st.lens = torch.tensor([cached], dtype=torch.int32, device="cuda")
+    poison(S, st, which, at)
+    q = st.rows([new], 4)
+    out = run(S, st, q, [new], [cached], max_new=new, t_hint=t_hint)
+    assert S.slim_last_launch_count() == 2 and int(st.status.item()) == 0
+    before = max(0, min(new, at - cached))
+    assert torch.isnan(out[before:]).all() and torch.isfinite(out[:before]).all()
+    check(st, q[:before], out[:before], [before], [cached])
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("dh,G,new", [(64, 1, 3), (64, 8, 3), (128, 4, 3)])
+def test_poisoned_page_few_rows(S, which, dh, G, new):
+    """The form for a few rows with the page alone in the last warp's share: only the row that attends it."""
+    cached = 4993 - new
+    st = PagedState(S, "e4m3", 1, dh, 16, [4993], [5000], seed=41)
+    st.lens = torch.tensor([cached], dtype=torch.int32, device="cuda")
+    poison(S, st, which, 4992)
+    q = st.rows([new], G)
+    out = run(S, st, q, [new], [cached], max_new=new)
+    assert S.slim_last_launch_count() == 2 and int(st.status.item()) == 0
+    assert torch.isnan(out[new - 1:]).all() and torch.isfinite(out[:new - 1]).all()
+    check(st, q[:new - 1], out[:new - 1], [new - 1], [cached])
