@@ -334,7 +334,9 @@ typedef struct slim_paged_cache {
  * scale where that is larger and the page held rows of the sequence before
  * (lens[b] lies inside the page). A larger scale re-rounds those older rows,
  * which changes only values that become subnormal in e4m3 (below 2^-6 of the
- * scale). New rows are rounded once. A key or value that is not finite makes
+ * scale). New rows are rounded once; under the largest scale, 2^120, what would
+ * round past bf16's range (from 248·2^120 on) becomes 240·2^120, so that finite
+ * rows read back finite. A key or value that is not finite makes
  * the page's scale NaN, and with it every output that attends a row of the page.
  *
  *   q        [rows][Hq][dh] bf16, row stride q_stride elements, or NULL

@@ -104,12 +104,21 @@ __device__ __forceinline__ uint4 pack8_bf16(const float* x) {
   return make_uint4(round_bf16x2(x[0], x[1]), round_bf16x2(x[2], x[3]), round_bf16x2(x[4], x[5]),
                     round_bf16x2(x[6], x[7]));
 }
-// Codes of 8 values; zeros under a NaN scale, so that only the scale carries it.
+// Codes of 8 values; zeros under a NaN scale, so that only the scale carries it. Under the largest scale
+// they stop at 240: the next code, 256, would stand for 2^128, which neither fp32 nor bf16 holds.
+// bf16's largest value, 255·2^120, stays within 2^-4 of its code (15/255).
 __device__ __forceinline__ uint2 pack8_e4m3(const float* x, float inv) {
   if (inv != inv) return make_uint2(0u, 0u);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
+  if (inv == exp2_int(-kScaleExpMax)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -240.f), 240.f);
+  }
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = to_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+  for (int i = 0; i < 4; ++i) w[i] = to_e4m3x2(y[2 * i], y[2 * i + 1]);
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 

@@ -75,7 +75,8 @@ class Pages:
                 if lo > 0:
                     s = max(s, self.scale[pid, h])
                     self.values[pid, h, :lo] = round_e4m3(self.values[pid, h, :lo] / s) * s
-                self.values[pid, h, lo:hi] = round_e4m3(x / s) * s
+                top = 240.0 if s == 2.0 ** EXP_MAX else 448.0  # 256·2^120 is past fp32 and bf16
+                self.values[pid, h, lo:hi] = round_e4m3(np.clip(x / s, -top, top)) * s
                 self.scale[pid, h] = s
 
     def read(self, table, n):

@@ -319,3 +319,52 @@ def test_offsets_past_32_bits(S, kind):
     step = 0.0 if kind == "bf16" else 2.0 ** -4
     for a, b in ((ko, k), (vo, v)):
         assert ((a.double() - b.double()).abs() <= step * b.double().abs() + step * 2.0 ** -6 * 2.0 ** -6).all()
+
+
+@pytest.mark.parametrize("n", [1, 3])
+def test_largest_magnitudes_read_back(S, n):
+    """Rows at bf16's largest magnitude, in both launch forms: their codes stand for finite values within a step's
+    half (2^-4) of them, read back and as outputs of both attentions."""
+    top = torch.finfo(torch.bfloat16).max
+    st = PagedState(S, "e4m3", 3, 64, 32, [0], [32], seed=9)
+    v = torch.zeros(n, 3, 64, dtype=torch.bfloat16, device="cuda")
+    v[:, 0] = top
+    v[:, 1] = -top
+    v[:, 2] = 247 * 2.0 ** 120  # the largest that rounds to 240·2^120
+    k = st.rows([n], 3)
+    S.slim_mha_paged_append(st.cache, k, v, st.starts([n]), st.lens, st.status, max_new=n)
+    ko, vo = torch.empty_like(v), torch.empty_like(v)
+    S.slim_mha_paged_gather(st.cache, st.lens, st.starts([n]), ko, vo, st.status)
+    q = st.rows([n], 3)
+    out = torch.empty_like(q)
+    S.slim_mha_paged_prefill(st.cache, q, st.starts([n]), st.lens, out,
+                             S.alloc_paged_prefill_workspace(st.cache, 3, n), st.status)
+    one = torch.empty_like(q[:1])
+    S.slim_mha_paged_decode(st.cache, q[:1], st.lens, one, S.alloc_paged_decode_workspace(st.cache, 3), st.status)
+    torch.cuda.synchronize()
+    assert int(st.status.item()) == 0 and (st.scales[1][int(st.table_h[0, 0])] == 2.0 ** 120).all()
+    for x in (vo, out, one):
+        assert torch.isfinite(x).all()
+        # an output is rounded to bf16 again, and its weights sum to 1 up to their rounding to f16
+        assert (np.abs(f64(x) / f64(v[:1]) - 1) <= 2.0 ** -4 + (0 if x is vo else 2.0 ** -8 + 2.0 ** -10)).all()
+
+
+def test_large_rows_beside_older_ones(S):
+    """A row at bf16's largest magnitude behind older rows: they keep their values, under a larger scale than theirs
+    and under the largest one."""
+    st = PagedState(S, "e4m3", 1, 64, 16, [0], [16], seed=10)
+    rows = torch.zeros(4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    rows[0] = 448 * 2.0 ** 119   # the largest code of the second largest scale
+    rows[1] = torch.finfo(torch.bfloat16).max
+    rows[2] = 240 * 2.0 ** 120
+    rows[3] = -torch.finfo(torch.bfloat16).max
+    lens = st.lens.clone()
+    for j in range(4):
+        S.slim_mha_paged_append(st.cache, rows[j:j + 1], rows[j:j + 1], st.starts([1]), lens, st.status)
+        lens += 1
+    ko, vo = torch.empty_like(rows), torch.empty_like(rows)
+    S.slim_mha_paged_gather(st.cache, st.lens, st.starts([4]), ko, vo, st.status)
+    torch.cuda.synchronize()
+    want = [448 * 2.0 ** 119, 240 * 2.0 ** 120, 240 * 2.0 ** 120, -240 * 2.0 ** 120]
+    for x in (ko, vo):
+        assert (f64(x) == np.array(want)[:, None, None]).all()
