@@ -325,9 +325,11 @@ class PagedKV:
 
 
 # The paged calls take microseconds on the GPU, so what the binding does per tensor counts: device
-# numbers instead of device objects, and the stream's handle without a Stream object around it.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# numbers instead of device objects, and the stream's handle without a Stream object around it. The
+# names that give them are private to torch and absent from some builds: the public functions stand in.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 
 def _on_device(t, name: str, dev: int, dtype, shape=None) -> int:

@@ -1,11 +1,16 @@
 """Host-side checks of the paged K+V cache calls (no GPU): every refusal comes before any launch."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
 import torch
 
 from oracle import paged_oracle as P
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -183,3 +188,20 @@ def test_oracle_grid():
     assert np.array_equal(P.round_e4m3(x.astype(np.float32)), torch_y)
     assert P.needed_scale(448.0) == 1 and P.needed_scale(448.0001) == 2 and P.needed_scale(224.0) == 0.5
     assert P.needed_scale(0.0) == 2.0 ** -100 and P.needed_scale(3e38) == 2.0 ** 120
+
+
+def test_import_without_private_torch_names():
+    """The module loads where torch lacks the private names that the paged calls take their stream and device from (a
+    build without CUDA, a later release), and then asks torch's public functions."""
+    code = ("import torch\n"
+            "for name in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "from only_cache_exact_b200 import slim\n"
+            "class Stream: cuda_stream = 77\n"
+            "torch.cuda.current_stream = lambda dev: Stream() if dev == 3 else None\n"
+            "torch.cuda.current_device = lambda: 3\n"
+            "got = []\n"
+            "slim._paged_call(lambda *a: got.append(a) or 0, 'call', 3, None, 1, 2)\n"
+            "assert got == [(1, 2, 77)], got\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
