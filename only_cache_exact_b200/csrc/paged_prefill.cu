@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   uint64_t* kempty = kfull + NK;   // [NK]
   uint64_t* vfull = kempty + NK;   // [NV]
   uint64_t* vempty = vfull + NV;   // [NV]
-  uint64_t* sfull = vempty + NV;   // [row tile][half] S written
+  uint64_t* sfull = vempty + NV;   // [row tile][half] S written (e4m3, first half: and the tile's scales)
   uint64_t* pready = sfull + 4;    // [row tile][half or part] P written over S (and O rescaled)
   uint64_t* pvdone = pready + 4;   // [row tile] a P·V completed
   uint64_t* ofull = pvdone + 2;    // [row tile] the tile's last P·V completed
@@ -190,7 +190,12 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
   int* s_bad = reinterpret_cast<int*>(tmem_slot + 1);  // first position whose page is outside the pool
   // e4m3: [key tile mod 8] for either half of the keys the scale of its pages if they share one (key scale,
   // value exponent, whether), then key scale and value exponent of each page. Written by the K producer before
-  // the tile's barrier.
+  // it arrives on the tile's kfull; the MMA warp that has waited for that arrives on the tile's first sfull
+  // beside the products, and so passes them on to the softmax warps (a commit alone orders the products, not
+  // what threads wrote. A barrier of their own for the scales took 4 % longer: one more wait in every tile).
+  // A slot is written again eight tiles later. No reader is that far behind: the rings are shorter, and a V
+  // stage comes free only with the P·V of every row tile that attends it, for which all its warps have read
+  // the scales and handed P over.
   float* s_scale = reinterpret_cast<float*>(bars + 64);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       mbar_init(&rempty[s], 4);
     }
     for (int t = 0; t < 4; ++t) {
-      mbar_init(&sfull[t], 1);
+      mbar_init(&sfull[t], E && (t & 1) == 0 ? 2 : 1);
       mbar_init(&pready[t], 4);
     }
     for (int t = 0; t < 8; ++t) mbar_init(&turn[t], 1);
@@ -414,6 +419,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
               umma_f16(d, qdesc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
             }
           }
+          if (E && hf == 0) mbar_arrive(&sfull[2 * t]);  // passes the tile's scales on
           umma_commit(&sfull[2 * t + hf]);
           if (hf == HV - 1 || u == steps - 1) release(&kempty[s], u / HV);
         }

@@ -503,3 +503,26 @@ def test_poisoned_page_few_rows(S, which, dh, G, new):
     assert S.slim_last_launch_count() == 2 and int(st.status.item()) == 0
     assert torch.isnan(out[new - 1:]).all() and torch.isfinite(out[:new - 1]).all()
     check(st, q[:new - 1], out[:new - 1], [new - 1], [cached])
+
+
+@pytest.mark.parametrize("dh,page,G,new", [(64, 16, 4, 200), (128, 32, 4, 70), (128, 128, 2, 300), (64, 64, 8, 16),
+                                           (128, 16, 8, 16), (64, 128, 4, 31)])
+@pytest.mark.parametrize("t_hint", [1, 0])
+def test_scales_of_many_pages(S, dh, page, G, new, t_hint):
+    """Every page has scales of its own over many key tiles, so that each tile's scales have to be that tile's: for
+    whole chunks, for one row tile (two key ranges), and split over CTAs."""
+    total = 3300
+    st = PagedState(S, "e4m3", 1, dh, page, [total], [total], seed=42)
+    for w in (0, 1):
+        f = np.exp2(st.rng.integers(-3, 4, size=(st.cache.num_pages, 1)))
+        st.scales[w].mul_(torch.from_numpy(f).to(torch.float32).cuda())
+        st.oracle[w].scale *= f
+        st.oracle[w].values *= f[:, :, None, None]
+    n, cached = [new], [total - new]
+    st.lens = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    q = st.rows(n, G)
+    want = run(S, st, q, n, cached, max_new=new, t_hint=t_hint)
+    check(st, q, want, n, cached)
+    for _ in range(20):
+        assert torch.equal(run(S, st, q, n, cached, max_new=new, t_hint=t_hint), want)
+    assert int(st.status.item()) == 0
