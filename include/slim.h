@@ -306,6 +306,16 @@ int slim_mha_decode_step(const float* q, const void* k_new, const void* v_new, v
  * keys and values of attended rows, must be finite; whatever lies in the pages
  * behind a sequence's rows is never used.
  *
+ * Precision of the attention calls: scores, sums and outputs are formed in fp32
+ * (bf16 values so large that their sum leaves fp32 overflow) and outputs rounded
+ * to bf16 once. Softmax weights are rounded for the products: SLIM_E4M3 to f16
+ * (2^-11), SLIM_BF16 to bf16 (2^-8) in slim_mha_paged_prefill, except that steps
+ * of up to 16 rows per key head (32 at dh = 64; max_new times Hq/Hkv) and
+ * slim_mha_paged_decode keep two bf16 parts (2^-16). The f16 weights have that
+ * precision for pages whose value scale is down to 2^21 below the largest one
+ * attended, weighed with its page's largest weight; below that they lose
+ * bits and at 2^32 vanish.
+ *
  * Return codes of all calls: SLIM_EINVAL for a null or misaligned pointer
  * (16 bytes), a size out of range or head counts that do not divide;
  * SLIM_EUNSUPPORTED for SLIM_F32, another dh, page or B > 4096.

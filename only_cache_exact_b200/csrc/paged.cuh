@@ -17,6 +17,13 @@ namespace slim {
 // left of a value that shares a row with ordinary ones.
 constexpr int kScaleExpMin = -100;
 constexpr int kScaleExpMax = 120;
+// Softmax weights over e4m3 are held in f16, at 2^7 times their size relative to the row's running maximum of
+// weight times value scale. That maximum may be 2^8 behind, so that they end at 2^15; upwards f16 has
+// no other use, and downwards a page may then hold its full 11 bits at a scale 2^21 below the largest one that
+// the row attends (one huge value row makes its page's scale so, whatever its own weight), and some at 2^31.
+// The sum of weights, which holds 2^-lv of scales from 2^-100 to 2^120, stays without that factor; the
+// output loses it with its last product.
+constexpr float kWeightLog2 = 7.f, kWeightInv = 0.0078125f;
 constexpr int kPagedMaxB = 4096;  // the decode plan holds one line offset per sequence in shared memory
 
 // Plain loads for everything an earlier kernel of the stream may have written (lengths, page tables,

@@ -7,8 +7,8 @@
 // o = Σ p_t V_t / Σ p_t, kept as a running (m, l, o) per warp and joined by
 // 2^(m_i - m). In e4m3 K_t = ks·k8_t and V_t = 2^lv·v8_t with scales of the page
 // and head: ks multiplies the score, and the weights of the sum over v8 are
-// P_t = 2^(s_t + lv - m) with m the running maximum of s + lv, which keeps them
-// in f16's range whatever the pages' scales are; l adds P_t·2^-lv.
+// P_t = 2^(s_t + lv - m + kWeightLog2) with m the running maximum of s + lv, which keeps
+// them in f16's range whatever the pages' scales are; l adds P_t·2^-(lv + kWeightLog2).
 //
 // Bound: memory. Each cached element is read once and meets 4 flops per row (a
 // query and head) for its 2 or 1 bytes; the row count of every matrix product
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
       }
     }
     float o[DH / 16][NT][4] = {};
-    float m[NT][2], neg_m[NT][2], l[NT][2];  // neg_m: -m, 0 while there is none
+    float m[NT][2], neg_m[NT][2], l[NT][2];  // neg_m: -m (e4m3: kWeightLog2 - m), 0 while there is none
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       m[n][0] = m[n][1] = -INFINITY, neg_m[n][0] = neg_m[n][1] = 0.f, l[n][0] = l[n][1] = 0.f;
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
           }
         }
       }
-      // Exponent of a weight: s·f + add, f the factor to log2 units, add = lv - m. Tiles that some row
+      // Exponent of a weight: s·f + add, f the factor to log2 units, add = lv + neg_m. Tiles that some row
       // does not attend whole (the last ones) are scaled and masked here, with f = 1 from then on.
       float f[C::kTT][NT][2], lv[C::kTT], fac[C::kTT];
       const bool full = (t + C::kTT) * 16 <= lim_all && tiles == C::kTT;
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
       for (int k = 0; k < C::kTT; ++k) {
         const float ks = E && k < tiles ? my_scale[(stage * C::kTT + k) * 2] : 1.f;
         lv[k] = E && k < tiles ? scale_log2(my_scale[(stage * C::kTT + k) * 2 + 1]) : 0.f;
-        fac[k] = E ? ex2(-lv[k]) : 1.f;
+        fac[k] = E ? ex2(-lv[k]) * kWeightInv : 1.f;  // subnormal for the largest scale: exact
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
           }
       }
       // A lane looks at its own scores only; the warp's maximum is taken when one of them exceeds the
-      // row's by more than 2^8 (weights up to that are harmless in f16 and bf16).
+      // row's by more than 2^8 (weights up to that fit f16, with 2^kWeightLog2, and bf16).
       float mx[NT][2];
       bool grow = false;
 #pragma unroll
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
             const float mn = fmaxf(m[n][i], x);
             const float alpha = mn == -INFINITY ? 1.f : ex2(m[n][i] - mn);
             m[n][i] = mn;
-            neg_m[n][i] = mn == -INFINITY ? 0.f : -mn;
+            neg_m[n][i] = mn == -INFINITY ? 0.f : E ? kWeightLog2 - mn : -mn;
             l[n][i] *= alpha;
 #pragma unroll
             for (int c = 0; c < DH / 16; ++c) {
@@ -562,14 +562,14 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
             if (E) low = low || fminf(x0, x1) < -60.f;
           }
           if (E) {
-            // the sum of p itself is that of P·2^-lv; taken from the scores where P may have underflowed
+            // the sum of p itself is that of P·2^-lv/2^kWeightLog2; taken from the scores where P may have underflowed
             if (__any_sync(0xffffffffu, low)) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const float z = fac[k] != fac[k] ? fac[k] : 0.f;  // a NaN scale stays
-                l[n][i] += ex2(fmaf(s[k][n][i], f[k][n][i], neg_m[n][i])) +
-                           ex2(fmaf(s[k][n][i + 2], f[k][n][i], neg_m[n][i])) + (e[i] != 0.f ? e[i] * z : 0.f) +
-                           (e[i + 2] != 0.f ? e[i + 2] * z : 0.f);
+                l[n][i] += (ex2(fmaf(s[k][n][i], f[k][n][i], neg_m[n][i])) +
+                            ex2(fmaf(s[k][n][i + 2], f[k][n][i], neg_m[n][i]))) * kWeightInv +
+                           (e[i] != 0.f ? e[i] * z : 0.f) + (e[i + 2] != 0.f ? e[i + 2] * z : 0.f);
               }
             } else {
 #pragma unroll
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
         for (int i = 0; i < 4; ++i) {
           const int hd = n * 8 + 2 * lq + (i & 1);
           if (hd >= nh) continue;
-          const float f = l[n][i & 1] > 0.f || l[n][i & 1] != l[n][i & 1] ? 1.f / l[n][i & 1] : 0.f;
+          const float f = l[n][i & 1] > 0.f || l[n][i & 1] != l[n][i & 1] ? (E ? kWeightInv : 1.f) / l[n][i & 1] : 0.f;
           int j;
           __nv_bfloat16* dst = p.out + row_of(r0g + hd, j) * DH;
 #pragma unroll
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(DecCfg<E, DH, NT>::kThreads, 1) paged_decode_k
 #pragma unroll
           for (int c = 0; c < DH / 16; ++c) {
             const int col = 16 * c + (E ? 2 * lg + (i >> 1) : lg + (i >> 1) * 8);
-            po[hd * DH + col] = o[c][n][i];
+            po[hd * DH + col] = E ? o[c][n][i] * kWeightInv : o[c][n][i];
           }
           if (lg == 0 && i < 2) {
             pm[hd * 2] = m[n][i];

@@ -22,8 +22,8 @@
 // e4m3 parts (high and low) that together hold a bf16 exactly: twice the products at twice the
 // rate of f16, and no key is converted. Value codes are exact in f16, and P·V runs in f16. The
 // key scale of a page multiplies its scores, the value scale 2^lv its probabilities,
-// P = 2^(s + lv - m) with m the running maximum of s + lv. P is rounded to f16 (2^-11) there;
-// over bf16 values it is rounded to bf16 (2^-8), the type the MMA wants beside them.
+// P = 2^(s + lv - m + kWeightLog2) with m the running maximum of s + lv. P is rounded to f16 (2^-11)
+// there; over bf16 values it is rounded to bf16 (2^-8), the type the MMA wants beside them.
 // Key rows at or past the sequence's end are zeroed in V before the first MMA
 // that reads them: a masked P = 0 never meets what a page held before.
 //
@@ -638,8 +638,9 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
       tmem_wait_ld();
       // Running maximum of the weights' exponents: of the scores in log2 units, for e4m3 plus the value
       // scale's exponent lv, so that P stays in f16's range whatever the pages' scales are. P of key t
-      // is 2^(s_t + e), e = lv - m, and l adds P·2^-lv. Where a group's largest P is below 2^-60 (its
+      // is 2^(s_t + e), e = lv - ref, and l adds P·2^-lv/2^kWeightLog2. Where a group's largest P is below 2^-60 (its
       // f16 is zero) e is raised to keep the fp32 sum from underflowing.
+      auto ref = [&]() { return m == -INFINITY ? 0.f : E ? m - kWeightLog2 : m; };
       auto advance = [&](float mt) {
         float alpha = 1.f;
         if (m == -INFINITY) {
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
         advance(mt + lvu);
         take_turn();
-        const float mm = m == -INFINITY ? 0.f : m;
+        const float mm = ref();
         float e = lvu - mm;
         if (E && mt != -INFINITY && e < -60.f - mt) e = -60.f - mt;
         float total = 0.f;
@@ -738,7 +739,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
           if (C::kParts == 2 && 32 * (q + 1) == C::kPart1) hand_over(0);
         }
         pass_turn();
-        l += E ? total * pf_ex2(-mm - e) : total;
+        l += E ? total * (pf_ex2(-mm - e) * kWeightInv) : total;
       } else {
         float fg[FH / 16], lv[FH / 16], mg[FH / 16], top = -INFINITY;
         const bool masked = __any_sync(0xffffffffu, k0 + FH - 1 > pos);
@@ -767,7 +768,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
         }
         advance(top);
         take_turn();
-        const float mm = m == -INFINITY ? 0.f : m;
+        const float mm = ref();
 #pragma unroll
         for (int q = 0; q < FH / 32; ++q) {
           float e[2], s2[2];
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
             if (e[k] < -60.f - x && x != -INFINITY) e[k] = -60.f - x;  // a NaN scale stays
           }
           weights(q, fg[2 * q], fg[2 * q + 1], e[0], e[1], s2[0], s2[1]);
-          l += s2[0] * pf_ex2(-mm - e[0]) + s2[1] * pf_ex2(-mm - e[1]);
+          l += s2[0] * (pf_ex2(-mm - e[0]) * kWeightInv) + s2[1] * (pf_ex2(-mm - e[1]) * kWeightInv);
           if (C::kParts == 2 && 32 * (q + 1) == C::kPart1) hand_over(0);
         }
         pass_turn();
@@ -811,7 +812,7 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
     };
     if (!kTwo && p.splits == 1) {
       if (q0 >= 0) {
-        const float inv = !got || broken || l == 0.f ? 0.f : 1.f / l;
+        const float inv = !got || broken || l == 0.f ? 0.f : (E ? kWeightInv : 1.f) / l;
 #pragma unroll 1
         for (int c = 0; c < DH; c += 64) {
           uint4 w[8];
@@ -848,6 +849,10 @@ __global__ void __launch_bounds__(PfCfg<E, DHB>::kThreads, 1)
             float v[16];
             tmem_ld16(tmem_o + lrow + static_cast<uint32_t>(c + 16 * g), v);
             tmem_wait_ld();
+            if (E) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] *= kWeightInv;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               w[4 * g + k] = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),

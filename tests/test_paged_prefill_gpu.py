@@ -526,3 +526,77 @@ def test_scales_of_many_pages(S, dh, page, G, new, t_hint):
     for _ in range(20):
         assert torch.equal(run(S, st, q, n, cached, max_new=new, t_hint=t_hint), want)
     assert int(st.status.item()) == 0
+
+
+@pytest.mark.parametrize("form", ["token", "few", "chunk"])
+@pytest.mark.parametrize("dh,page", [(64, 16), (128, 128)])
+@pytest.mark.parametrize("ratio", [12, 20, 26])
+def test_one_huge_value_row(S, form, dh, page, ratio):
+    """A value row 2^ratio times the others that hardly counts (its weight is below 2^-100) makes its page's scale as
+    much larger, and its neighbours, which do count, zeros. The weights are held in f16 relative to the largest
+    weight times page scale: every other page's are that much smaller. With P = 2^7·2^(s + lv - m) an f16 weight
+    is off by at most 2^-25 where it is subnormal (2^-11 of it otherwise), so that the sum over value codes v8 is
+    off by at most 2^-25·2^-7·max_t(p_t 2^lv_t)·Σ|v8_t|, beside the bound for ordinary pages."""
+    n = {"token": 1, "few": 3, "chunk": 100}[form]
+    total = 700
+    st = PagedState(S, "e4m3", 1, dh, page, [0], [total], seed=43)
+    k, v = st.rows([total], 1, 0.5), st.rows([total], 1)
+    k[:, :, 0] = 0
+    k[200, 0, 0] = -30.0 * dh ** 0.5
+    v[200] *= 2.0 ** ratio
+    S.slim_mha_paged_append(st.cache, k, v, st.starts([total]), st.lens, st.status)
+    st.lens += total - n
+    for w in (0, 1):
+        st.oracle[w].values = np.nan_to_num(st.values(w), nan=0.0)
+    q = st.rows([n], 4)
+    q[:, :, 0] = 4.0
+    if form == "token":
+        out = torch.empty_like(q)
+        S.slim_mha_paged_decode(st.cache, q, st.lens, out, S.alloc_paged_decode_workspace(st.cache, 4), st.status)
+        torch.cuda.synchronize()
+    else:
+        out = run(S, st, q, [n], [total - n], max_new=n)
+    assert int(st.status.item()) == 0
+    K, V = (st.oracle[w].read(st.table_h[0], total) for w in (0, 1))
+    lv = np.repeat(f64(st.scales[1])[st.table_h[0, :-(-total // page)], 0], page)[:total]
+    o, A, D = P.attend(f64(q), K, V, [total - n + j for j in range(n)])
+    for j in range(n):
+        T = total - n + j + 1
+        z = f64(q[j]) @ K[:T, 0].T / dh ** 0.5
+        p = np.exp(z - z.max(axis=1, keepdims=True))
+        p /= p.sum(axis=1, keepdims=True)
+        assert (p[:, 200] < 2.0 ** -100).all()
+        under = (p * lv[:T]).max(axis=1)[:, None] * np.abs(V[:T, 0] / lv[:T, None]).sum(axis=0) * 2.0 ** -32
+        err = np.abs(f64(out[j]) - o[j])
+        assert (err <= bound("e4m3", dh, o[j], A[j], D[j]) + under).all(), (j, (err / A[j]).max())
+
+
+@pytest.mark.parametrize("form", ["token", "few", "chunk"])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("t_hint", [1, 0])
+def test_zero_values_before_ordinary_ones(S, form, page, t_hint):
+    """Thousands of rows whose values are zero (pages of the smallest scale, 2^-100), most of them with scores 2^7.5
+    above those of the first ones, and then a few with ordinary values: the sum of weights holds both."""
+    n = {"token": 1, "few": 3, "chunk": 100}[form]
+    total, dh = 17 * 512, 64
+    st = PagedState(S, "e4m3", 1, dh, page, [0], [total], seed=44)
+    k, v = st.rows([total], 1, 0.02), st.rows([total], 1)
+    k[:, :, 0] = 7.5 * np.log(2.0) * dh ** 0.5 / 4
+    k[:64, :, 0] = 0
+    v[:-128] = 0
+    S.slim_mha_paged_append(st.cache, k, v, st.starts([total]), st.lens, st.status)
+    st.lens += total - n
+    for w in (0, 1):
+        st.oracle[w].values = np.nan_to_num(st.values(w), nan=0.0)
+    assert (f64(st.scales[1])[st.table_h[0, 0]] == 2.0 ** -100).all()
+    q = st.rows([n], 2)
+    q[:, :, 0] = 4.0
+    if form == "token":
+        out = torch.empty_like(q)
+        S.slim_mha_paged_decode(st.cache, q, st.lens, out, S.alloc_paged_decode_workspace(st.cache, 2), st.status,
+                                t_hint=t_hint)
+        torch.cuda.synchronize()
+    else:
+        out = run(S, st, q, [n], [total - n], max_new=n, t_hint=t_hint)
+    assert int(st.status.item()) == 0
+    check(st, q, out, [n], [total - n])
