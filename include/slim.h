@@ -410,8 +410,9 @@ int slim_mha_paged_decode(const slim_paged_cache* cache, const void* q, int64_t 
  *   q          [rows][Hq][dh] bf16, row stride q_stride elements (rotated)
  *   Hq         a multiple of Hkv, at most 128·Hkv and 8192
  *   t_hint     host-side estimate of the longest lens[b] + new rows, used only
- *              to choose how work is split (<= 0 means cap). The workspace call
- *              takes the same value.
+ *              to choose how work is split (<= 0 means cap, which costs parts
+ *              that find little to do where sequences are far shorter). The
+ *              workspace call takes the same value.
  *   out        [rows][Hq][dh] bf16 contiguous
  *   workspace  >= slim_mha_paged_prefill_workspace_bytes(...), 256-byte aligned
  *              (may be NULL where that is 0)

@@ -1,6 +1,6 @@
 // Attention of a few query rows per sequence over a paged K+V cache in bf16 or
 // e4m3: slim_mha_paged_decode (one row), and slim_mha_paged_prefill where the
-// rows that share a key head are at most 32 (a few proposed tokens).
+// rows that share a key head are at most 16, 32 at dh = 64 (a few proposed tokens).
 //
 // Mathematics, per sequence and key/value head, for the G query heads that
 // share it: s_t = q·K_t·log2(e)/sqrt(dh), m = max s, p_t = 2^(s_t - m),
@@ -26,7 +26,8 @@
 // Work split: 16-row tiles of all (sequence, head group) pairs on one line, cut
 // in equal shares for the CTAs and, inside, for their warps; a warp streams its
 // tiles through its own ring in shared memory (cp.async, no barrier with other
-// warps): 192 KB of rings per SM, two thirds or more of it in flight. Partials of
+// warps): 192 KB of rings per SM. All stages but the one being worked on are in flight: two thirds of
+// the ring or more, but half with 8 rows over e4m3 at dh = 128 (12 warps, two stages each). Partials of
 // warps that end in one sequence are joined in the CTA; what a sequence has in
 // other CTAs is joined by merge_paged_kernel. Small calls take one CTA per
 // (sequence, head group) instead and need no merge.
